@@ -79,6 +79,22 @@ class QkvParams(C.Structure):
     ]
 
 
+class Kv4Cache(C.Structure):
+    _fields_ = [
+        ("k_pages", vp), ("k_page_scales", vp), ("k_tensor_scale", vp),
+        ("v_pages", vp), ("v_page_scales", vp), ("v_tensor_scale", vp),
+        ("num_pages", i32), ("kv_heads", i32), ("head_dim", i32),
+    ]
+
+
+class Kv4Tokens(C.Structure):
+    _fields_ = [
+        ("cache", Kv4Cache), ("k", vp), ("v", vp), ("k_stride", i64), ("v_stride", i64),
+        ("dtype", i32), ("total", i32), ("cu", vp), ("start", vp), ("page_table", vp),
+        ("num_seqs", i32), ("max_pages", i32),
+    ]
+
+
 #: name -> (restype, argtypes); exactly the functions include/qk4v8.h declares.
 SIGNATURES = {
     "qk4v8_version": (C.c_int, []),
@@ -104,6 +120,14 @@ SIGNATURES = {
     "attn_qk4v8_decode_paged": (i32, [C.POINTER(DecodeParams), vp, sz, vp]),
     "attn_qk4v8_decode_paged_noalloc": (i32, [C.POINTER(DecodeParams), vp]),
     "kv_append_paged": (i32, [C.POINTER(AppendParams), vp]),
+    "kv4_append_paged": (i32, [C.POINTER(Kv4Tokens), vp]),
+    "kv4_read_paged": (i32, [C.POINTER(Kv4Tokens), vp]),
+    "kv_pages_workspace_size": (sz, [i32, i32]),
+    "kv_pages_alloc": (i32, [vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
+    "kv_pages_fork": (i32, [vp, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]),
+    "kv_pages_free": (i32, [vp, i32, vp, i32, i32, vp, vp, i32, vp]),
+    "kv_pages_compact": (i32, [vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+    "kv_pages_copy": (i32, [C.POINTER(vp), C.POINTER(i64), i32, i32, vp, vp, i32, vp, vp]),
 }
 
 _LIB = None

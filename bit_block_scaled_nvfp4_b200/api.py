@@ -62,6 +62,12 @@ def _on_one_gpu(*ts) -> None:
             raise ValueError("the library takes contiguous tensors on one CUDA device")
 
 
+def _same_gpu(first, *ts) -> None:
+    for t in ts:
+        if not t.is_cuda or t.get_device() != first.get_device():
+            raise ValueError("the library takes tensors on one CUDA device")
+
+
 def _nvfp4_empty(shape, device, want_fp16: bool = False) -> NVFP4Tensor:
     """Uninitialised NVFP4 output for an input of ``shape`` (..., D)."""
     lead, cols = tuple(shape[:-1]), shape[-1]
@@ -536,6 +542,217 @@ def kv_append_paged(cache: PagedKV, k_new: torch.Tensor, v_new: torch.Tensor,
         kv_heads=hkv, head_dim=d, max_new=int(max_new))
     st = lib.kv_append_paged(C.byref(p), _stream())
     _lib.check(st, "kv_append_paged")
+
+
+# ---- the 4-bit cache ----
+@dataclass
+class PagedKV4:
+    """Paged cache with K and V both in NVFP4 (64-token pages; qk4v8_kv4_cache)."""
+    k_pages: torch.Tensor        # [P, Hkv, 64, D/2]
+    k_scales: torch.Tensor       # [P, Hkv, 64, D/16]
+    k_tensor_scale: torch.Tensor  # [1] float
+    v_pages: torch.Tensor        # [P, Hkv, 32, D]   byte c of row i: tokens 2i (low nibble), 2i + 1
+    v_scales: torch.Tensor       # [P, Hkv, D/16, 64]
+    v_tensor_scale: torch.Tensor  # [1] float
+
+
+def _kv4_cache(cache: PagedKV4):
+    """The cache's struct and its buffers, after checking their shapes against one another."""
+    _expect_dims(cache.k_pages, "cache.k_pages", 4, "[P, Hkv, 64, D/2]")
+    P, hkv, _, dh = cache.k_pages.shape
+    d = dh * 2
+    _expect(cache.k_pages, "cache.k_pages", (P, hkv, 64, d // 2), torch.uint8)
+    _expect(cache.k_scales, "cache.k_scales", (P, hkv, 64, d // 16), torch.uint8)
+    _expect_scalar(cache.k_tensor_scale, "cache.k_tensor_scale")
+    _expect(cache.v_pages, "cache.v_pages", (P, hkv, 32, d), torch.uint8)
+    _expect(cache.v_scales, "cache.v_scales", (P, hkv, d // 16, 64), torch.uint8)
+    _expect_scalar(cache.v_tensor_scale, "cache.v_tensor_scale")
+    bufs = [cache.k_pages, cache.k_scales, cache.k_tensor_scale,
+            cache.v_pages, cache.v_scales, cache.v_tensor_scale]
+    c = _lib.Kv4Cache(k_pages=_ptr(cache.k_pages), k_page_scales=_ptr(cache.k_scales),
+                      k_tensor_scale=_ptr(cache.k_tensor_scale), v_pages=_ptr(cache.v_pages),
+                      v_page_scales=_ptr(cache.v_scales), v_tensor_scale=_ptr(cache.v_tensor_scale),
+                      num_pages=P, kv_heads=hkv, head_dim=d)
+    return c, bufs
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the tokens of t [T, H, D]: tokens may be strided (a slice of a wider
+    projection), heads and channels have to be contiguous and tokens must not overlap."""
+    T, h, d = t.shape
+    stride = t.stride(0) if T > 1 else max(t.stride(0), h * d)
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d) or stride < h * d):
+        raise ValueError(f"{name}: heads and channels must be contiguous, tokens apart from one another")
+    if stride % 8:
+        if T > 1:
+            raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart")
+        stride = h * d
+    return stride
+
+
+def _kv4_tokens(cache: PagedKV4, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor,
+                start: torch.Tensor, page_table: torch.Tensor):
+    _expect_dims(k, "k", 3, "[total, Hkv, D]")
+    _expect_dims(page_table, "page_table", 2, "[S, max_pages]")
+    c, bufs = _kv4_cache(cache)
+    total, S = k.shape[0], page_table.shape[0]
+    _expect(k, "k", (total, c.kv_heads, c.head_dim), k.dtype)
+    _expect(v, "v", tuple(k.shape), k.dtype)
+    _expect(cu, "cu", (S + 1,), torch.int32)
+    _expect(start, "start", (S,), torch.int32)
+    _expect(page_table, "page_table", tuple(page_table.shape), torch.int32)
+    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
+    _on_one_gpu(*bufs, cu, start, page_table)
+    _same_gpu(cu, k, v)
+    return _lib.Kv4Tokens(cache=c, k=_ptr(k), v=_ptr(v), k_stride=ks, v_stride=vs,
+                          dtype=_OUT_DT[k.dtype], total=total, cu=_ptr(cu), start=_ptr(start),
+                          page_table=_ptr(page_table), num_seqs=S, max_pages=page_table.shape[1])
+
+
+def kv4_append_paged(cache: PagedKV4, k_new: torch.Tensor, v_new: torch.Tensor, cu_new: torch.Tensor,
+                     lens: torch.Tensor, page_table: torch.Tensor) -> None:
+    """Quantize new tokens into the 4-bit cache in place. k_new, v_new [total_new, Hkv, D]
+    (fp16/bf16; tokens may be strided); cu_new [S + 1] int32 offsets of each sequence's rows;
+    lens [S] int32 lengths before the call (the caller adds the new counts); page_table
+    [S, max_pages] int32."""
+    _dtype(k_new)
+    p = _kv4_tokens(cache, k_new, v_new, cu_new, lens, page_table)
+    with torch.cuda.device(lens.device):
+        _lib.check(_lib.load().kv4_append_paged(C.byref(p), _stream()), "kv4_append_paged")
+
+
+def kv4_read_paged(cache: PagedKV4, cu: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor,
+                   total: int, dtype=torch.bfloat16, out=None):
+    """Read cached tokens back: the values of positions start[s] .. of every sequence s,
+    cu[s + 1] - cu[s] of them, packed as k, v [total, Hkv, D] in ``dtype`` (fp16, bf16 or fp32).
+    ``out``: optional (k, v) to write into; rows behind the last sequence keep what they hold."""
+    if dtype not in _OUT_DT:
+        raise TypeError(f"expected fp16, bf16 or fp32, got {dtype}")
+    if out is None:
+        hkv, d = cache.k_pages.shape[1], cache.k_pages.shape[3] * 2
+        k = torch.empty(total, hkv, d, dtype=dtype, device=start.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        if k.shape[0] != total or k.dtype != dtype:
+            raise ValueError(f"out: expected {total} rows of {dtype}")
+    p = _kv4_tokens(cache, k, v, cu, start, page_table)
+    with torch.cuda.device(start.device):
+        _lib.check(_lib.load().kv4_read_paged(C.byref(p), _stream()), "kv4_read_paged")
+    return k, v
+
+
+# ---- page pool ----
+@dataclass
+class PageMoves:
+    """Pages to copy inside a cache: src[i] -> dst[i], -1 for none (int32 device tensors); with
+    ``count`` ([1] int32) only the first count of them. ``seq_src`` / ``seq_dst``: after a fork,
+    the sequences forked, for state kept per sequence. From kv_pages_fork, kv_pages_compact or
+    paged.page_moves, which give no destination twice and none that is also a source."""
+    src: torch.Tensor
+    dst: torch.Tensor
+    num_pages: int
+    count: torch.Tensor | None = None
+    seq_src: torch.Tensor | None = None
+    seq_dst: torch.Tensor | None = None
+
+
+def _pool_args(pool, page_table: torch.Tensor, lens: torch.Tensor, *more):
+    _expect_dims(page_table, "page_table", 2, "[S, max_pages]")
+    S = page_table.shape[0]
+    _expect(pool.refs, "pool.refs", (pool.refs.numel(),), torch.int32)
+    _expect(page_table, "page_table", tuple(page_table.shape), torch.int32)
+    _expect(lens, "lens", (S,), torch.int32)
+    for name, t in more:
+        _expect(t, name, (t.numel(),), torch.int32)
+    _on_one_gpu(pool.refs, page_table, lens, *[t for _, t in more])
+    return (_ptr(pool.refs), pool.refs.numel(), _ptr(page_table), S, page_table.shape[1], _ptr(lens))
+
+
+def _pool_workspace(pool, page_table):
+    n = _lib.load().kv_pages_workspace_size(pool.refs.numel(), page_table.shape[0])
+    return torch.empty(n, dtype=torch.uint8, device=pool.refs.device)
+
+
+def kv_pages_alloc(pool, page_table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor) -> None:
+    """Give every sequence the pages it needs to grow from lens[s] to new_lens[s] tokens, lowest
+    free pages first (page_table and pool.refs updated in place; lens is not: append, then
+    advance it). All or nothing: see kv_pages_alloc in include/qk4v8.h."""
+    args = _pool_args(pool, page_table, lens, ("new_lens", new_lens))
+    if new_lens.numel() != lens.numel():
+        raise ValueError("new_lens must have one entry per sequence")
+    ws = _pool_workspace(pool, page_table)
+    with torch.cuda.device(lens.device):
+        _lib.check(_lib.load().kv_pages_alloc(*args, _ptr(new_lens), _ptr(ws), ws.numel(), _stream()),
+                   "kv_pages_alloc")
+
+
+def kv_pages_fork(pool, page_table: torch.Tensor, lens: torch.Tensor, src: torch.Tensor,
+                  dst: torch.Tensor) -> PageMoves:
+    """Fork sequence src[i] into the empty sequence dst[i] (int32 device tensors): full pages are
+    shared, a last page that is not full gets a page of its own. Returns the page copies to
+    make: pass them to kv_pages_copy for every layer's cache before anything is appended."""
+    args = _pool_args(pool, page_table, lens, ("src", src), ("dst", dst))
+    n = src.numel()
+    if dst.numel() != n:
+        raise ValueError("src and dst must have the same number of sequences")
+    ws = _pool_workspace(pool, page_table)
+    with torch.cuda.device(lens.device):
+        m = torch.empty(4, n, dtype=torch.int32, device=lens.device)
+        _lib.check(_lib.load().kv_pages_fork(*args, _ptr(src), _ptr(dst), n, _ptr(m[0]), _ptr(m[1]),
+                                             _ptr(m[2]), _ptr(m[3]), _ptr(ws), ws.numel(), _stream()),
+                   "kv_pages_fork")
+    return PageMoves(m[0], m[1], pool.refs.numel(), None, m[2], m[3])
+
+
+def kv_pages_free(pool, page_table: torch.Tensor, lens: torch.Tensor, seqs: torch.Tensor) -> None:
+    """Drop the sequences seqs[i] (int32 device tensor): their pages' counts fall, their table
+    entries become -1 and their lengths 0."""
+    args = _pool_args(pool, page_table, lens, ("seqs", seqs))
+    with torch.cuda.device(lens.device):
+        _lib.check(_lib.load().kv_pages_free(*args, _ptr(seqs), seqs.numel(), _stream()), "kv_pages_free")
+
+
+def kv_pages_compact(pool, page_table: torch.Tensor, lens: torch.Tensor) -> PageMoves:
+    """Renumber the pages so that the live ones are the lowest; page_table and pool.refs follow.
+    Returns the page copies to make: pass them to kv_pages_copy for every layer's cache before
+    the tables are used again."""
+    args = _pool_args(pool, page_table, lens)
+    P = pool.refs.numel()
+    ws = _pool_workspace(pool, page_table)
+    with torch.cuda.device(lens.device):
+        m = torch.empty(2 * (P // 2 + 1) + 1, dtype=torch.int32, device=lens.device)
+        src, dst, count = m[:P // 2 + 1], m[P // 2 + 1:-1], m[-1:]
+        _lib.check(_lib.load().kv_pages_compact(*args, _ptr(src), _ptr(dst), _ptr(count), _ptr(ws),
+                                                ws.numel(), _stream()), "kv_pages_compact")
+    return PageMoves(src, dst, P, count)
+
+
+def _copy_rows(arrays, src, dst, rows: int, count, where: str) -> None:
+    _on_one_gpu(*arrays, src, dst, count)
+    n = len(arrays)
+    ptrs = (C.c_void_p * n)(*[a.data_ptr() for a in arrays])
+    size = (C.c_int64 * n)(*[a.numel() // rows * a.element_size() for a in arrays])
+    with torch.cuda.device(src.device):
+        _lib.check(_lib.load().kv_pages_copy(ptrs, size, n, rows, _ptr(src), _ptr(dst), src.numel(),
+                                             _ptr(count), _stream()), where)
+
+
+def kv_pages_copy(cache, moves: PageMoves) -> None:
+    """Copy the moved pages' contents inside ``cache`` (a PagedKV4 or a PagedKV)."""
+    arrays = [cache.k_pages, cache.k_scales, cache.v_pages, cache.v_scales]
+    for a in arrays:
+        if a.shape[0] != moves.num_pages:
+            raise ValueError(f"the cache has {a.shape[0]} pages, the moves are of {moves.num_pages}")
+    _copy_rows(arrays, moves.src, moves.dst, moves.num_pages, moves.count, "kv_pages_copy")
+
+
+def kv_tails_copy(v_tail: torch.Tensor, moves: PageMoves) -> None:
+    """After a fork, the forked sequences' incomplete V groups (kv_append_paged's v_tail
+    [S, Hkv, D, 32] of a PagedKV), copied to the sequences forked into."""
+    if moves.seq_src is None:
+        raise ValueError("moves of a fork are needed")
+    _copy_rows([v_tail], moves.seq_src, moves.seq_dst, v_tail.shape[0], None, "kv_tails_copy")
 
 
 def qk4v8_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,

@@ -1,0 +1,203 @@
+// The 4-bit paged cache: tokens quantized into it and read back. K and V in NVFP4, every token on
+// its own (quantize.cuh's block arithmetic with the cache's fixed tensor scales); layout in
+// include/qk4v8.h.
+//
+// One thread per (token, KV head, 16-channel block). V bytes hold two tokens, so the thread of
+// an even position writes both tokens' nibbles when the odd one is new too, and a token whose
+// neighbour is not part of the call keeps the neighbour's nibble; no two threads write one byte.
+// A CTA's 256 threads cover consecutive rows; the first row's sequence is found by counting the
+// offsets not past it (all threads, one pass over cu), later rows walk on from there.
+#pragma once
+#include "quantize.cuh"
+
+namespace qk4v8 {
+
+struct Kv4Cache {
+  uint8_t* k_pages;
+  uint8_t* k_scales;
+  const float* k_ts;
+  uint8_t* v_pages;
+  uint8_t* v_scales;
+  const float* v_ts;
+  int32_t num_pages, Hkv;
+};
+
+struct Kv4TokensArgs {
+  Kv4Cache c;
+  void* k;
+  void* v;
+  int64_t k_stride, v_stride;
+  const int32_t* cu;
+  const int32_t* start;
+  const int32_t* page_table;
+  int32_t total, S, max_pages;
+};
+
+constexpr int kKv4D = 128, kKv4Blocks = kKv4D / 16;   // head dimension; scale blocks a token
+
+// Number of cu[1..S] not past `row` = the sequence of that row (S when it is behind the last),
+// by every thread of the CTA.
+__device__ __forceinline__ int kv4_seq_of_row(const int32_t* cu, int S, int row) {
+  int n = 0;
+  for (int i0 = 0; i0 < S; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x;
+    n += __syncthreads_count(i < S && cu[i + 1] <= row);
+  }
+  return n;
+}
+
+// A token's place in the cache: physical page and slot. false (and the status word set) when it
+// has none.
+struct Kv4Place {
+  int page, slot;
+};
+__device__ __forceinline__ bool kv4_place(const Kv4TokensArgs& a, int s, int pos, bool flag,
+                                          Kv4Place& pl) {
+  if (a.start[s] < 0 || pos < 0 || (pos >> 6) >= a.max_pages) {
+    if (flag) flag_error(kStatusBounds);
+    return false;
+  }
+  pl.page = a.page_table[static_cast<int64_t>(s) * a.max_pages + (pos >> 6)];
+  pl.slot = pos & 63;
+  if (pl.page < 0 || pl.page >= a.c.num_pages) {
+    if (flag) flag_error(kStatusBounds);
+    return false;
+  }
+  return true;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t kv4_encode_block(const T* src, float s_t, uint32_t* w) {
+  const uint4* p = reinterpret_cast<const uint4*>(src);
+  float f[16];
+  unpack8<T>(__ldg(p), f);
+  unpack8<T>(__ldg(p + 1), f + 8);
+  return nvfp4_encode16(f, s_t, w);
+}
+// Eight nibbles -> the low nibbles of eight bytes.
+__device__ __forceinline__ uint2 nibbles_to_bytes(uint32_t w) {
+  uint32_t lo = w & 0xFFFFu, hi = w >> 16;
+  lo = (lo | (lo << 8)) & 0x00FF00FFu;
+  hi = (hi | (hi << 8)) & 0x00FF00FFu;
+  return make_uint2((lo | (lo << 4)) & 0x0F0F0F0Fu, (hi | (hi << 4)) & 0x0F0F0F0Fu);
+}
+
+// The row of this thread, its sequence and position; false when it has none.
+struct Kv4Job {
+  int row, s, pos, last, h, b;      // last: the row is its sequence's last
+};
+__device__ __forceinline__ bool kv4_job(const Kv4TokensArgs& a, Kv4Job& j) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x;
+  const int per_row = a.c.Hkv * kKv4Blocks;
+  int s = kv4_seq_of_row(a.cu, a.S, static_cast<int>(first / per_row));
+  const int64_t i = first + threadIdx.x;
+  const int64_t row = i / per_row;
+  if (row >= a.total) return false;
+  const int rest = static_cast<int>(i - row * per_row);
+  j.row = static_cast<int>(row);
+  j.h = rest / kKv4Blocks;
+  j.b = rest % kKv4Blocks;
+  while (s < a.S && a.cu[s + 1] <= j.row) ++s;
+  if (s >= a.S || a.cu[s] > j.row) return false;      // behind the last sequence
+  j.s = s;
+  // 64 bits: a start near the top of 32 bits must not wrap to a valid position
+  const int64_t pos = static_cast<int64_t>(a.start[s]) + (j.row - a.cu[s]);
+  j.pos = pos > 0x7fffffff ? -1 : static_cast<int>(pos);
+  j.last = j.row + 1 >= a.cu[s + 1] || j.row + 1 >= a.total;
+  return true;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) kv4_append_kernel(Kv4TokensArgs a) {
+  Kv4Job j;
+  if (!kv4_job(a, j)) return;
+  Kv4Place pl;
+  if (!kv4_place(a, j.s, j.pos, true, pl)) return;
+  const int64_t head = static_cast<int64_t>(pl.page) * a.c.Hkv + j.h;
+  const int64_t in = j.h * kKv4D + j.b * 16;
+  uint32_t w[2];
+  {
+    const uint32_t sc = kv4_encode_block<T>(static_cast<const T*>(a.k) + j.row * a.k_stride + in, *a.c.k_ts, w);
+    const int64_t tok = head * 64 + pl.slot;
+    *reinterpret_cast<uint2*>(a.c.k_pages + tok * (kKv4D / 2) + j.b * 8) = make_uint2(w[0], w[1]);
+    a.c.k_scales[tok * kKv4Blocks + j.b] = static_cast<uint8_t>(sc);
+  }
+  const bool odd = pl.slot & 1;
+  if (odd && j.row > a.cu[j.s]) return;                // written by the even token's thread
+  const T* vr = static_cast<const T*>(a.v) + j.row * a.v_stride + in;
+  uint4* dst = reinterpret_cast<uint4*>(a.c.v_pages + (head * 32 + (pl.slot >> 1)) * kKv4D + j.b * 16);
+  uint8_t* sdst = a.c.v_scales + (head * kKv4Blocks + j.b) * 64 + pl.slot;
+  uint32_t o[4];
+  sdst[0] = static_cast<uint8_t>(kv4_encode_block<T>(vr, *a.c.v_ts, w));
+  const uint2 c0 = nibbles_to_bytes(w[0]), c1 = nibbles_to_bytes(w[1]);
+  o[0] = c0.x; o[1] = c0.y; o[2] = c1.x; o[3] = c1.y;
+  if (odd || j.last) {                                 // the pair's other token is not new
+    const uint4 old = *dst;
+    const uint32_t* ow = reinterpret_cast<const uint32_t*>(&old);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = odd ? (ow[i] & 0x0F0F0F0Fu) | (o[i] << 4) : (ow[i] & 0xF0F0F0F0u) | o[i];
+  } else {
+    sdst[1] = static_cast<uint8_t>(kv4_encode_block<T>(vr + a.v_stride, *a.c.v_ts, w));
+    const uint2 d0 = nibbles_to_bytes(w[0]), d1 = nibbles_to_bytes(w[1]);
+    o[0] |= d0.x << 4; o[1] |= d0.y << 4; o[2] |= d1.x << 4; o[3] |= d1.y << 4;
+  }
+  *dst = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Two values v0, v1 -> one packed word of T (16-bit types).
+template <typename T> __device__ __forceinline__ uint32_t pack2(float v0, float v1);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float v0, float v1) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(v0, v1);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float v0, float v1) {
+  const __half2 t = __floats2half2_rn(v0, v1);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* dst, const float* f) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<float4*>(dst)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4TokensArgs a) {
+  Kv4Job j;
+  if (!kv4_job(a, j)) return;
+  Kv4Place pl;
+  if (!kv4_place(a, j.s, j.pos, true, pl)) return;
+  const int64_t head = static_cast<int64_t>(pl.page) * a.c.Hkv + j.h;
+  const int64_t in = j.h * kKv4D + j.b * 16;
+  const int64_t tok = head * 64 + pl.slot;
+  const uint2 kc = *reinterpret_cast<const uint2*>(a.c.k_pages + tok * (kKv4D / 2) + j.b * 8);
+  const uint4 vc = *reinterpret_cast<const uint4*>(a.c.v_pages + (head * 32 + (pl.slot >> 1)) * kKv4D + j.b * 16);
+  // code * scale has at most six significant bits: exact; one rounding by the tensor scale
+  const float ks = e4m3_code_to_float(a.c.k_scales[tok * kKv4Blocks + j.b]);
+  const float vs = e4m3_code_to_float(a.c.v_scales[(head * kKv4Blocks + j.b) * 64 + pl.slot]);
+  const float kt = *a.c.k_ts, vt = *a.c.v_ts;
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w = i < 8 ? kc.x : kc.y;
+    f[i] = __fmul_rn(e2m1_value((w >> (4 * (i & 7))) & 0xFu) * ks, kt);
+  }
+  store16<T>(static_cast<T*>(a.k) + j.row * a.k_stride + in, f);
+  const uint32_t* vw = reinterpret_cast<const uint32_t*>(&vc);
+  const int sh = 4 * (pl.slot & 1);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    f[i] = __fmul_rn(e2m1_value((vw[i >> 2] >> (8 * (i & 3) + sh)) & 0xFu) * vs, vt);
+  store16<T>(static_cast<T*>(a.v) + j.row * a.v_stride + in, f);
+}
+
+}  // namespace qk4v8

@@ -13,6 +13,8 @@
 #include "attn_pp.cuh"
 #include "decode.cuh"
 #include "append.cuh"
+#include "kv4.cuh"
+#include "pages.cuh"
 
 using namespace qk4v8;
 
@@ -116,6 +118,8 @@ size_t qk4v8_struct_size(int32_t which) {
          : which == 1 ? sizeof(qk4v8_decode_params)
          : which == 2 ? sizeof(qk4v8_append_params)
          : which == 3 ? sizeof(qk4v8_qkv_params)
+         : which == 4 ? sizeof(qk4v8_kv4_cache)
+         : which == 5 ? sizeof(qk4v8_kv4_tokens)
                       : 0;
 }
 
@@ -782,4 +786,162 @@ extern "C" qk4v8_status quantize_nvfp4_residual(const void* x, qk4v8_dtype dtype
                                                 uint8_t* scales2, cudaStream_t stream) {
   return quantize_nvfp4_residual_impl(x, dtype, rows, cols, row_stride, codes, scales,
                                       tensor_scale, codes2, scales2, stream);
+}
+
+// ------------------------------------------------------------------------------------------
+// The 4-bit cache (kv4.cuh)
+// ------------------------------------------------------------------------------------------
+static qk4v8_status check_kv4_cache(const qk4v8_kv4_cache& c) {
+  if (!c.k_pages || !c.k_page_scales || !c.k_tensor_scale || !c.v_pages || !c.v_page_scales || !c.v_tensor_scale)
+    return QK4V8_ERR_INVALID_ARG;
+  if (c.num_pages <= 0 || c.kv_heads <= 0) return QK4V8_ERR_INVALID_ARG;
+  if (c.head_dim != kKv4D) return QK4V8_ERR_UNSUPPORTED;
+  if (!aligned(c.k_pages, 16) || !aligned(c.k_page_scales, 16) || !aligned(c.v_pages, 16) ||
+      !aligned(c.v_page_scales, 16) || !aligned(c.k_tensor_scale, 4) || !aligned(c.v_tensor_scale, 4))
+    return QK4V8_ERR_INVALID_ARG;
+  return QK4V8_OK;
+}
+static Kv4Cache kv4_cache(const qk4v8_kv4_cache& c) {
+  return Kv4Cache{c.k_pages, c.k_page_scales, c.k_tensor_scale, c.v_pages, c.v_page_scales, c.v_tensor_scale,
+                  c.num_pages, c.kv_heads};
+}
+
+// Checks of both token calls; `grid` gets the CTAs to launch (0: nothing to do).
+static qk4v8_status check_kv4_tokens(const qk4v8_kv4_tokens* p, bool f32, Kv4TokensArgs* a, unsigned* grid) {
+  if (p == nullptr || !p->cu || !p->start || !p->page_table) return QK4V8_ERR_INVALID_ARG;
+  if (const qk4v8_status st = check_kv4_cache(p->cache); st != QK4V8_OK) return st;
+  if (p->dtype != QK4V8_F16 && p->dtype != QK4V8_BF16 && !(f32 && p->dtype == QK4V8_F32))
+    return QK4V8_ERR_INVALID_ARG;
+  if (p->total < 0 || p->num_seqs <= 0 || p->max_pages <= 0) return QK4V8_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(p->cache.kv_heads) * kKv4D;
+  if (p->k_stride < row || p->v_stride < row || p->k_stride % 8 || p->v_stride % 8) return QK4V8_ERR_INVALID_ARG;
+  *grid = 0;
+  if (p->total == 0) return QK4V8_OK;
+  if (!p->k || !p->v || !aligned(p->k, 16) || !aligned(p->v, 16)) return QK4V8_ERR_INVALID_ARG;
+  const int64_t jobs = static_cast<int64_t>(p->total) * p->cache.kv_heads * kKv4Blocks;
+  if ((jobs + 255) / 256 > 0x7fffffffLL) return QK4V8_ERR_UNSUPPORTED;
+  *grid = static_cast<unsigned>((jobs + 255) / 256);
+  *a = Kv4TokensArgs{kv4_cache(p->cache), p->k, p->v, p->k_stride, p->v_stride, p->cu, p->start, p->page_table,
+                     p->total, p->num_seqs, p->max_pages};
+  return QK4V8_OK;
+}
+
+extern "C" qk4v8_status kv4_append_paged(const qk4v8_kv4_tokens* p, cudaStream_t stream) {
+  Kv4TokensArgs a;
+  unsigned grid;
+  const qk4v8_status st = check_kv4_tokens(p, false, &a, &grid);
+  if (st != QK4V8_OK || grid == 0) return st;
+  if (p->dtype == QK4V8_BF16) kv4_append_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
+  else kv4_append_kernel<__half><<<grid, 256, 0, stream>>>(a);
+  return launch_status();
+}
+
+extern "C" qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* p, cudaStream_t stream) {
+  Kv4TokensArgs a;
+  unsigned grid;
+  const qk4v8_status st = check_kv4_tokens(p, true, &a, &grid);
+  if (st != QK4V8_OK || grid == 0) return st;
+  if (p->dtype == QK4V8_BF16) kv4_read_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
+  else if (p->dtype == QK4V8_F16) kv4_read_kernel<__half><<<grid, 256, 0, stream>>>(a);
+  else kv4_read_kernel<float><<<grid, 256, 0, stream>>>(a);
+  return launch_status();
+}
+
+// ------------------------------------------------------------------------------------------
+// Page pool (pages.cuh). Workspace: num_seqs + 1 ints, one for the live count, 2 * num_pages.
+// ------------------------------------------------------------------------------------------
+extern "C" size_t kv_pages_workspace_size(int32_t num_pages, int32_t num_seqs) {
+  if (num_pages <= 0 || num_seqs < 0) return 0;
+  return 4 * (static_cast<size_t>(num_seqs) + 2 + 2 * static_cast<size_t>(num_pages));
+}
+
+static qk4v8_status check_pool(const void* refs, int32_t num_pages, const void* table, int32_t num_seqs,
+                               int32_t max_pages, const void* lens, const void* ws, size_t ws_bytes,
+                               bool need_ws) {
+  if (!refs || !table || !lens || num_pages <= 0 || num_seqs <= 0 || max_pages <= 0) return QK4V8_ERR_INVALID_ARG;
+  if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4)) return QK4V8_ERR_INVALID_ARG;
+  if (num_pages > 0x7fffffff - 8192) return QK4V8_ERR_UNSUPPORTED;   // a pass's last indexes stay in 32 bits
+  if (need_ws && (!ws || !aligned(ws, 4) || ws_bytes < kv_pages_workspace_size(num_pages, num_seqs)))
+    return QK4V8_ERR_INVALID_ARG;
+  return QK4V8_OK;
+}
+
+extern "C" qk4v8_status kv_pages_alloc(int32_t* refs, int32_t num_pages, int32_t* page_table, int32_t num_seqs,
+                                       int32_t max_pages, const int32_t* lens, const int32_t* new_lens,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const qk4v8_status st = check_pool(refs, num_pages, page_table, num_seqs, max_pages, lens, workspace, workspace_bytes, true);
+  if (st != QK4V8_OK) return st;
+  if (!new_lens) return QK4V8_ERR_INVALID_ARG;
+  int32_t* off = static_cast<int32_t*>(workspace);
+  pages_alloc_kernel<<<1, kPoolThreads, 0, stream>>>(refs, num_pages, page_table, num_seqs, max_pages, lens, new_lens,
+                                                     off, off + num_seqs + 2);
+  return launch_status();
+}
+
+extern "C" qk4v8_status kv_pages_fork(int32_t* refs, int32_t num_pages, int32_t* page_table, int32_t num_seqs,
+                                      int32_t max_pages, int32_t* lens, const int32_t* src, const int32_t* dst,
+                                      int32_t n, int32_t* move_src, int32_t* move_dst, int32_t* seq_src,
+                                      int32_t* seq_dst, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const qk4v8_status st = check_pool(refs, num_pages, page_table, num_seqs, max_pages, lens, workspace, workspace_bytes, true);
+  if (st != QK4V8_OK) return st;
+  if (n < 0) return QK4V8_ERR_INVALID_ARG;
+  if (n == 0) return QK4V8_OK;
+  if (!src || !dst || !move_src || !move_dst || !seq_src || !seq_dst) return QK4V8_ERR_INVALID_ARG;
+  if (n > 0x7fffffff - kPoolThreads) return QK4V8_ERR_UNSUPPORTED;
+  int32_t* claim = static_cast<int32_t*>(workspace);
+  pages_fork_kernel<<<1, kPoolThreads, 0, stream>>>(refs, num_pages, page_table, num_seqs, max_pages, lens, src, dst, n,
+                                                    move_src, move_dst, seq_src, seq_dst, claim, claim + num_seqs + 2);
+  return launch_status();
+}
+
+extern "C" qk4v8_status kv_pages_free(int32_t* refs, int32_t num_pages, int32_t* page_table, int32_t num_seqs,
+                                      int32_t max_pages, int32_t* lens, const int32_t* seqs, int32_t n,
+                                      cudaStream_t stream) {
+  const qk4v8_status st = check_pool(refs, num_pages, page_table, num_seqs, max_pages, lens, nullptr, 0, false);
+  if (st != QK4V8_OK) return st;
+  if (n < 0) return QK4V8_ERR_INVALID_ARG;
+  if (n == 0) return QK4V8_OK;
+  if (!seqs) return QK4V8_ERR_INVALID_ARG;
+  pages_free_kernel<<<n, 128, 0, stream>>>(refs, num_pages, page_table, num_seqs, max_pages, lens, seqs);
+  return launch_status();
+}
+
+extern "C" qk4v8_status kv_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table, int32_t num_seqs,
+                                         int32_t max_pages, const int32_t* lens, int32_t* move_src,
+                                         int32_t* move_dst, int32_t* move_count, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream) {
+  const qk4v8_status st = check_pool(refs, num_pages, page_table, num_seqs, max_pages, lens, workspace, workspace_bytes, true);
+  if (st != QK4V8_OK) return st;
+  if (!move_src || !move_dst || !move_count) return QK4V8_ERR_INVALID_ARG;
+  int32_t* n_live = static_cast<int32_t*>(workspace);
+  int32_t* holes = n_live + num_seqs + 2;
+  int32_t* map = holes + num_pages;
+  pages_compact_kernel<<<1, kPoolThreads, 0, stream>>>(refs, num_pages, move_src, move_dst, move_count, n_live, holes, map);
+  if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
+  pages_remap_kernel<<<num_seqs, 128, 0, stream>>>(num_pages, page_table, max_pages, lens, n_live, map);
+  return launch_status();
+}
+
+extern "C" qk4v8_status kv_pages_copy(void* const* arrays, const int64_t* page_bytes, int32_t n_arrays,
+                                      int32_t num_pages, const int32_t* src, const int32_t* dst, int32_t n,
+                                      const int32_t* count, cudaStream_t stream) {
+  if (!arrays || !page_bytes || n_arrays < 1 || n_arrays > kMaxPageArrays || num_pages <= 0 || n < 0)
+    return QK4V8_ERR_INVALID_ARG;
+  PageCopyArgs a;
+  int64_t words = 0;
+  for (int i = 0; i < n_arrays; ++i) {
+    if (!arrays[i] || !aligned(arrays[i], 16) || page_bytes[i] <= 0 || page_bytes[i] % 16) return QK4V8_ERR_INVALID_ARG;
+    a.base[i] = static_cast<uint4*>(arrays[i]);
+    a.words[i] = page_bytes[i] / 16;
+    words += a.words[i];
+    a.end[i] = words;
+  }
+  if (n == 0) return QK4V8_OK;
+  if (!src || !dst) return QK4V8_ERR_INVALID_ARG;
+  if ((words + 1023) / 1024 > 0x7fffffffLL) return QK4V8_ERR_UNSUPPORTED;
+  a.n_arrays = n_arrays; a.num_pages = num_pages; a.n = n;
+  a.src = src; a.dst = dst; a.count = count;
+  const dim3 grid(static_cast<unsigned>((words + 1023) / 1024), static_cast<unsigned>(n < 1024 ? n : 1024));
+  pages_copy_kernel<<<grid, 256, 0, stream>>>(a);
+  return launch_status();
 }

@@ -48,7 +48,8 @@ int qk4v8_version(void);
 
 /* sizeof the parameter structs, for bindings that mirror them: which = 0 gives
  * sizeof(qk4v8_fwd_params), 1 sizeof(qk4v8_decode_params), 2 sizeof(qk4v8_append_params),
- * 3 sizeof(qk4v8_qkv_params), anything else 0. */
+ * 3 sizeof(qk4v8_qkv_params), 4 sizeof(qk4v8_kv4_cache), 5 sizeof(qk4v8_kv4_tokens),
+ * anything else 0. */
 size_t qk4v8_struct_size(int32_t which);
 
 /* Human-readable name of a status code (static string). */
@@ -394,6 +395,120 @@ typedef struct {
 } qk4v8_append_params;
 
 qk4v8_status kv_append_paged(const qk4v8_append_params* params, cudaStream_t stream);
+
+/*
+ * The 4-bit paged cache: K and V both in NVFP4 (E2M1 codes, one E4M3 scale per 16 channels of a
+ * token, one FP32 scale per tensor; the quantize_nvfp4 arithmetic with a fixed tensor scale).
+ * Every token is quantized on its own, so a cache can be appended to, cut back and forked at any
+ * token and needs no state besides its pages. 144 bytes a token and KV head at head_dim 128.
+ * Pages hold 64 tokens:
+ *   k_pages       [num_pages, Hkv, 64, D/2]   channel 2i of a token in the low nibble of byte i
+ *   k_page_scales [num_pages, Hkv, 64, D/16]
+ *   v_pages       [num_pages, Hkv, 32, D]     byte c of row i: channel c of token 2i (low nibble)
+ *                                             and of token 2i + 1 (high nibble)
+ *   v_page_scales [num_pages, Hkv, D/16, 64]
+ * (V's byte pairs two tokens because tokens are the contraction axis of P V: one conversion
+ * gives two neighbours along it.) All buffers 16-byte aligned; head_dim must be 128.
+ */
+typedef struct {
+  uint8_t* k_pages;
+  uint8_t* k_page_scales;
+  const float* k_tensor_scale; /* device scalar, > 0 */
+  uint8_t* v_pages;
+  uint8_t* v_page_scales;
+  const float* v_tensor_scale; /* device scalar, > 0 */
+  int32_t num_pages, kv_heads, head_dim;
+} qk4v8_kv4_cache;
+
+/*
+ * kv4_append_paged — quantize new tokens into the 4-bit cache.
+ * kv4_read_paged   — the reverse: the same tokens' values, code * scale * tensor scale in FP32,
+ *                    rounded once to `dtype` (F16, BF16 or F32).
+ * For sequence s the tokens are rows cu[s] .. cu[s+1]-1 of k / v and take positions
+ * start[s] .. start[s] + n_s - 1 (n_s = cu[s+1] - cu[s] >= 0); position t lives in physical page
+ * page_table[s][t / 64], slot t % 64. Rows at or past cu[S] are neither read nor written, and
+ * nothing but the tokens' own codes and scales is written (the other nibble of a shared V byte
+ * keeps its value).
+ * k, v       [total, Hkv, D], heads and channels contiguous, a token k_stride / v_stride elements
+ *            after the one before it (>= Hkv * D, a multiple of 8: K and V may be slices of one
+ *            projection's output), 16-byte aligned. Append reads F16 or BF16.
+ * cu         [S + 1] int32, cu[0] = 0, nondecreasing.
+ * start      [S] int32 (not modified; after an append the caller advances its lengths).
+ * page_table [S, max_pages] int32.
+ * No page may hold slots of two sequences that a call writes (fork with kv_pages_fork, which
+ * gives each sequence its own last page).
+ * Device checks: a negative start, a position at or past 64 * max_pages or a page id outside
+ * [0, num_pages) sets QK4V8_ERR_BOUNDS (qk4v8_check_status) and that token is skipped (a read
+ * leaves its output rows as they were).
+ */
+typedef struct {
+  qk4v8_kv4_cache cache;
+  void* k;
+  void* v;
+  int64_t k_stride, v_stride;  /* elements from one token to the next */
+  qk4v8_dtype dtype;
+  int32_t total;               /* rows of k and v */
+  const int32_t* cu;
+  const int32_t* start;
+  const int32_t* page_table;
+  int32_t num_seqs, max_pages;
+} qk4v8_kv4_tokens;
+
+qk4v8_status kv4_append_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream);
+qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream);
+
+/*
+ * Page pool: which pages of a cache (of either kind; all layers of a model share one page table)
+ * are in use. refs [num_pages] int32 counts the sequences that hold each page, 0 = free. A
+ * sequence of length n holds the first ceil(n / 64) entries of its page-table row. Every call
+ * that takes free pages takes the lowest-numbered ones, in order of the sequences given, so the
+ * state after a call depends on nothing but the state before it. refs, page_table [S, max_pages]
+ * and lens [S] are updated in place on the device; no call reads anything back.
+ * A call whose arguments cannot be met as a whole (a sequence id out of range, too few free
+ * pages, a length past 64 * max_pages, ...) changes nothing and sets QK4V8_ERR_BOUNDS.
+ *
+ * kv_pages_alloc    pages for growing from lens[s] to new_lens[s] (>= lens[s]) tokens, for every
+ *                   s; lens is not modified (append, then advance it).
+ * kv_pages_fork     sequence src[i] forked into the empty sequence dst[i] (lens[dst] == 0; all
+ *                   dst distinct, none its own src), i < n: full pages are shared, a last page that is not
+ *                   full is to be copied into a page of dst's own. Writes the copies to make to
+ *                   move_src / move_dst [n] (-1 where there is none) and, for per-sequence state
+ *                   kept beside the pages (kv_append_paged's v_tail), the forks made to
+ *                   seq_src / seq_dst [n] (-1 everywhere when the call is refused).
+ * kv_pages_free     sequences seqs[i] dropped: their pages' counts fall, their row entries become -1
+ *                   and lens 0. A sequence that is empty, or named twice, is freed once. An id
+ *                   or page out of range, or a page nobody holds, is skipped (QK4V8_ERR_BOUNDS).
+ * kv_pages_compact  live pages moved into [0, number of live pages): the i-th live page past
+ *                   that goes to the i-th hole before it. Page tables and refs follow; the moves are
+ *                   written to move_src / move_dst [num_pages / 2 + 1] and their number to
+ *                   move_count [1].
+ * kv_pages_copy     page src[i] of each of n_arrays (1..8) arrays copied to page dst[i], i < n
+ *                   (and < *count, when count is not NULL); entries of -1 are skipped. Array a
+ *                   has num_pages pages of page_bytes[a] bytes (a multiple of 16; 16-byte
+ *                   aligned). No dst may be given twice or also be a src. arrays and page_bytes
+ *                   are HOST arrays.
+ * workspace  >= kv_pages_workspace_size(num_pages, num_seqs) bytes, 4-byte aligned.
+ */
+size_t kv_pages_workspace_size(int32_t num_pages, int32_t num_seqs);
+qk4v8_status kv_pages_alloc(int32_t* refs, int32_t num_pages, int32_t* page_table,
+                            int32_t num_seqs, int32_t max_pages, const int32_t* lens,
+                            const int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+qk4v8_status kv_pages_fork(int32_t* refs, int32_t num_pages, int32_t* page_table,
+                           int32_t num_seqs, int32_t max_pages, int32_t* lens, const int32_t* src,
+                           const int32_t* dst, int32_t n, int32_t* move_src, int32_t* move_dst,
+                           int32_t* seq_src, int32_t* seq_dst, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+qk4v8_status kv_pages_free(int32_t* refs, int32_t num_pages, int32_t* page_table, int32_t num_seqs,
+                           int32_t max_pages, int32_t* lens, const int32_t* seqs, int32_t n,
+                           cudaStream_t stream);
+qk4v8_status kv_pages_compact(int32_t* refs, int32_t num_pages, int32_t* page_table,
+                              int32_t num_seqs, int32_t max_pages, const int32_t* lens,
+                              int32_t* move_src, int32_t* move_dst, int32_t* move_count,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+qk4v8_status kv_pages_copy(void* const* arrays, const int64_t* page_bytes, int32_t n_arrays,
+                           int32_t num_pages, const int32_t* src, const int32_t* dst, int32_t n,
+                           const int32_t* count, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

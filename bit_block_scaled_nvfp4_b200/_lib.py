@@ -95,6 +95,15 @@ class Kv4Tokens(C.Structure):
     ]
 
 
+class Kv4AttnParams(C.Structure):
+    _fields_ = [
+        ("cache", Kv4Cache), ("q", vp), ("q_stride", i64), ("dtype", i32), ("total_q", i32),
+        ("cu_q", vp), ("context_lens", vp), ("page_table", vp),
+        ("num_seqs", i32), ("max_pages", i32), ("q_heads", i32), ("max_q", i32),
+        ("max_context", i32), ("softmax_scale", f32), ("out", vp), ("lse", vp),
+    ]
+
+
 #: name -> (restype, argtypes); exactly the functions include/qk4v8.h declares.
 SIGNATURES = {
     "qk4v8_version": (C.c_int, []),
@@ -122,6 +131,8 @@ SIGNATURES = {
     "kv_append_paged": (i32, [C.POINTER(AppendParams), vp]),
     "kv4_append_paged": (i32, [C.POINTER(Kv4Tokens), vp]),
     "kv4_read_paged": (i32, [C.POINTER(Kv4Tokens), vp]),
+    "attn_kv4_paged_workspace_size": (sz, [C.POINTER(Kv4AttnParams)]),
+    "attn_kv4_paged": (i32, [C.POINTER(Kv4AttnParams), vp, sz, vp]),
     "kv_pages_workspace_size": (sz, [i32, i32]),
     "kv_pages_alloc": (i32, [vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
     "kv_pages_fork": (i32, [vp, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]),

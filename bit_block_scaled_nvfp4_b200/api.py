@@ -642,6 +642,127 @@ def kv4_read_paged(cache: PagedKV4, cu: torch.Tensor, start: torch.Tensor, page_
     return k, v
 
 
+def _kv4_attn_params(q: torch.Tensor, cache: PagedKV4, page_table: torch.Tensor,
+                     context_lens: torch.Tensor, max_context: int, cu_q, max_q: int,
+                     softmax_scale, out: torch.Tensor, lse):
+    """The attention parameter struct, after checking every buffer against the sizes it states."""
+    _expect_dims(q, "q", 3, "[T, Hq, D]")
+    _expect_dims(page_table, "page_table", 2, "[S, max_pages]")
+    c, bufs = _kv4_cache(cache)
+    T, hq, d = q.shape
+    S = page_table.shape[0]
+    _expect(q, "q", (T, hq, c.head_dim), q.dtype)
+    _expect(page_table, "page_table", tuple(page_table.shape), torch.int32)
+    _expect(context_lens, "context_lens", (S,), torch.int32)
+    _expect(out, "out", (T, hq, d), q.dtype)
+    bufs += [page_table, context_lens, out]
+    if cu_q is not None:
+        _expect(cu_q, "cu_q", (S + 1,), torch.int32)
+        bufs.append(cu_q)
+    elif T != S or max_q != 1:
+        raise ValueError("without cu_q, q holds one token per sequence")
+    if lse is not None:
+        _expect(lse, "lse", (T, hq), torch.float32)
+        bufs.append(lse)
+    stride = _token_stride(q, "q")
+    dt = _dtype(q)
+    _on_one_gpu(*bufs)
+    _same_gpu(page_table, q)
+    return _lib.Kv4AttnParams(
+        cache=c, q=_ptr(q), q_stride=stride, dtype=dt, total_q=T, cu_q=_ptr(cu_q),
+        context_lens=_ptr(context_lens), page_table=_ptr(page_table), num_seqs=S,
+        max_pages=page_table.shape[1], q_heads=hq, max_q=int(max_q), max_context=int(max_context),
+        softmax_scale=1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale,
+        out=_ptr(out), lse=_ptr(lse))
+
+
+def _kv4_workspace(p, workspace, device):
+    need = _lib.load().attn_kv4_paged_workspace_size(C.byref(p))
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes (uint8)")
+    _on_one_gpu(workspace)
+    if workspace.device != device:
+        raise ValueError("the library takes tensors on one CUDA device")
+    return workspace
+
+
+def attn_kv4_paged(q: torch.Tensor, cache: PagedKV4, page_table: torch.Tensor,
+                   context_lens: torch.Tensor, max_context: int, cu_q: torch.Tensor | None = None,
+                   max_q: int = 1, softmax_scale: float | None = None, want_lse: bool = False,
+                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Causal attention of 16-bit queries over the 4-bit cache: a decoding step, proposed tokens,
+    chunks of prompts or whole prompts, in any mixture. q [T, Hq, D] (fp16/bf16; tokens may be
+    strided) holds sequence s's tokens in rows cu_q[s] .. cu_q[s + 1] - 1, at most ``max_q`` of
+    them and the last of its context; without ``cu_q`` one token per sequence. context_lens [S]
+    counts them in (append them first), ``max_context`` bounds it. Returns out [T, Hq, D] in q's
+    type (and lse [T, Hq])."""
+    _expect_dims(q, "q", 3, "[T, Hq, D]")
+    dev = q.device
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if want_lse else None
+    p = _kv4_attn_params(q, cache, page_table, context_lens, max_context, cu_q, max_q,
+                         softmax_scale, out, lse)
+    with torch.cuda.device(dev):
+        ws = _kv4_workspace(p, workspace, dev)
+        _lib.check(_lib.load().attn_kv4_paged(C.byref(p), _ptr(ws), ws.numel(), _stream()), "attn_kv4_paged")
+    return (out, lse) if want_lse else out
+
+
+class KV4AttentionPlan:
+    """attn_kv4_paged for serving loops: the fixed buffers (cache, page table, context lengths,
+    outputs for up to ``max_tokens`` query tokens, workspace) are checked and allocated once;
+    ``run(q, cu_q)`` checks the step's queries and launches, and returns views of the plan's own
+    outputs (read them before the next ``run``)."""
+
+    def __init__(self, cache: PagedKV4, page_table: torch.Tensor, context_lens: torch.Tensor,
+                 max_context: int, q_heads: int, max_q: int = 1, max_tokens: int | None = None,
+                 dtype=torch.bfloat16, softmax_scale: float | None = None, want_lse: bool = False,
+                 workspace: torch.Tensor | None = None):
+        dev, d = cache.k_pages.device, cache.k_pages.shape[3] * 2
+        S = page_table.shape[0]
+        self._seqs = S
+        self._max_q = int(max_q)
+        self.max_tokens = S * self._max_q if max_tokens is None else int(max_tokens)
+        self.out = torch.empty(self.max_tokens, q_heads, d, dtype=dtype, device=dev)
+        self.lse = torch.empty(self.max_tokens, q_heads, dtype=torch.float32, device=dev) if want_lse else None
+        probe_cu = torch.empty(S + 1, dtype=torch.int32, device=dev)
+        self.params = _kv4_attn_params(self.out, cache, page_table, context_lens, max_context, probe_cu,
+                                       max_q, softmax_scale, self.out, self.lse)
+        with torch.cuda.device(dev):
+            self.workspace = _kv4_workspace(self.params, workspace, dev)
+        self._keep = (cache, page_table, context_lens)
+        self._shape, self._dtype = (q_heads, d), dtype
+        self._dev = self.out.get_device()
+
+    def run(self, q: torch.Tensor, cu_q: torch.Tensor | None = None):
+        """One step for q [T, Hq, D], T <= max_tokens; without cu_q one token per sequence."""
+        T = q.shape[0]
+        if q.dim() != 3 or tuple(q.shape[1:]) != self._shape or q.dtype != self._dtype or \
+                T > self.max_tokens or not q.is_cuda or q.get_device() != self._dev:
+            raise ValueError(f"q must be up to {self.max_tokens} tokens of {self._shape} {self._dtype} on the plan's device")
+        p = self.params
+        if cu_q is None:
+            if T != self._seqs or self._max_q != 1:
+                raise ValueError("without cu_q, q holds one token per sequence")
+            p.cu_q = None
+        else:
+            _expect(cu_q, "cu_q", (self._seqs + 1,), torch.int32)
+            if not cu_q.is_cuda or cu_q.get_device() != self._dev or not cu_q.is_contiguous():
+                raise ValueError("cu_q must be contiguous on the plan's device")
+            p.cu_q = cu_q.data_ptr()
+        p.q, p.q_stride, p.total_q = q.data_ptr(), _token_stride(q, "q"), T
+        if torch.cuda.current_device() == self._dev:
+            st = _lib.load().attn_kv4_paged(C.byref(p), _ptr(self.workspace), self.workspace.numel(), _stream())
+        else:
+            with torch.cuda.device(self._dev):
+                st = _lib.load().attn_kv4_paged(C.byref(p), _ptr(self.workspace), self.workspace.numel(), _stream())
+        _lib.check(st, "attn_kv4_paged")
+        return (self.out[:T], self.lse[:T]) if self.lse is not None else self.out[:T]
+
+
 # ---- page pool ----
 @dataclass
 class PageMoves:

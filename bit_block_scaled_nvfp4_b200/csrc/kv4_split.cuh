@@ -1,0 +1,547 @@
+// Attention of few query rows per KV head over the 4-bit cache (decoding steps, proposed tokens):
+// split over the keys, plus the merge of the splits.
+//
+// Mathematics: for the n query tokens of a sequence and one KV head, the R = n g rows (token,
+// head of the group) see the same keys. S^T = K Q^T and O^T += V^T P^T on 16-bit tensor cores with
+// FP32 accumulators; K and V are E2M1 x E4M3 products of at most six significant bits between
+// 2^-10 and 2688, exact in fp16. Q is scaled per row by a power of two into fp16's range (exact
+// but for elements 2^-20 below the row's largest) and the factor goes into the softmax constant.
+// P = 2^(s - m + 6) is rounded to fp16 (2^-12 relative; the 2^6 keeps weights down to 2^-20
+// of the largest out of the subnormals); m, l and O are FP32, l sums the unrounded weights.
+//
+// Bound: the cache is read once, 144 bytes a token and KV head, and everything is laid out so
+// that codes go from shared memory into tensor-core operands without being moved between threads:
+//   * keys are the M dimension of both products (16 tokens or 16 channels a tile), rows the N
+//     dimension (8 a tile), so a decoding step of g <= 8 wastes nothing on padding rows to 16;
+//   * a thread of the K operand needs pairs of neighbouring channels of a token: a byte of the
+//     page. The order of channels is free as long as Q has the same one: thread t of four takes
+//     channels 32 t .. 32 t + 31, one 16-byte load;
+//   * a thread of the V^T operand needs pairs of neighbouring tokens of a channel: a byte of the
+//     page too, since V's bytes pair tokens. Thread c of eight takes channels 16 c .. 16 c + 15, one
+//     16-byte load and one scale block;
+//   * P^T has to change from accumulator to operand layout: one 8x8 transpose a tile (movmatrix).
+// The tensor-core form is mma.sync: operands come from registers, where the decoding leaves
+// them; through shared or tensor memory every decoded byte would be written and read again.
+//
+// Work split: the pages of all (sequence, KV head) pairs form one line, cut into equal
+// consecutive ranges, one a CTA, whatever the lengths. A CTA's eight warps take half a page each
+// (four pages at a time), each with its own running maximum, and are merged through shared memory
+// where a pair ends. A pair inside one CTA is written out; one that crosses CTAs leaves
+// partials (O, m, l) that the merge kernel joins. A ninth warp brings pages in by bulk copies.
+#pragma once
+#include <type_traits>
+#include "kv4.cuh"
+#include "attn_fwd.cuh"
+
+namespace qk4v8 {
+
+struct Kv4AttnArgs {
+  Kv4Cache c;
+  const void* q;
+  int64_t q_stride;
+  const int32_t* cu_q;       // or null: one token a sequence
+  const int32_t* lens;
+  const int32_t* table;
+  int32_t total_q, S, max_pages, Hq, max_q, max_context;
+  int32_t rows_max;          // the split kernel takes sequences of at most this many rows a KV head
+  float softmax_scale;
+  void* out;
+  float* lse;
+  int32_t* plan;             // workspace: [0] units a CTA, [1 + s] first unit of sequence s
+  float* part;               // workspace: partials, two a CTA
+};
+
+constexpr float kPShift = 6.f;
+constexpr uint32_t kKernelKv4Split = 4;
+
+struct Kv4Seq {
+  int q0, n, ctx;            // first query row, query tokens, context
+};
+// Sequence s as the caller gave it; n = 0 when it has no query tokens or is out of range.
+__device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool flag) {
+  Kv4Seq q;
+  q.q0 = a.cu_q ? a.cu_q[s] : s;
+  q.n = a.cu_q ? a.cu_q[s + 1] - q.q0 : 1;
+  q.ctx = a.lens[s];
+  if (q.n == 0) return q;
+  if (q.n < 0 || q.n > a.max_q || q.q0 < 0 || q.q0 > a.total_q - q.n || q.ctx < q.n ||
+      q.ctx > a.max_context || ((q.ctx - 1) >> 6) >= a.max_pages) {
+    if (flag) flag_error(kStatusBounds);
+    q.n = 0;
+  }
+  return q;
+}
+
+// One (sequence, KV head) pair's part of a CTA's range: pages [p0, p1) of np.
+struct Kv4Seg {
+  int s, h, p0, p1, np;
+  Kv4Seq q;
+};
+// Walks a CTA's range of units (a unit: one page of one KV head), sequence by sequence, head by head.
+struct Kv4Walk {
+  int s, h, p, left;         // next unit, units left
+  __device__ __forceinline__ bool next(const Kv4AttnArgs& a, Kv4Seg& g) {
+    if (left <= 0) return false;
+    const int group = a.Hq / a.c.Hkv;
+    for (;; ++s) {
+      if (s >= a.S) return false;
+      g.q = kv4_seq(a, s, false);
+      if (g.q.n > 0 && g.q.n * group <= a.rows_max) break;
+    }
+    g.s = s; g.h = h; g.p0 = p;
+    g.np = (g.q.ctx + 63) >> 6;
+    g.p1 = min(g.np, p + left);
+    left -= g.p1 - p;
+    p = 0;
+    if (++h == a.c.Hkv) { h = 0; ++s; }
+    return true;
+  }
+};
+
+template <int NT>
+struct Kv4SplitLayout {
+  static constexpr int WARPS = 8, THREADS = WARPS * 32 + 32;
+  static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
+  static constexpr int NS = NT == 1 ? 8 : 16;           // ring stages of one page
+  static constexpr int ROWS = NT * 8;
+  static constexpr int STAGE = 9216, OFF_V = 4096, OFF_KS = 8192, OFF_VS = 8704;
+  static constexpr int Q_LD = 272;                      // bytes of a Q row (256 + 16)
+  static constexpr int M_LD = 132;                      // floats of a merge row (128 + 4)
+  static constexpr int OFF_Q = NS * STAGE;
+  static constexpr int OFF_M = OFF_Q + ROWS * Q_LD;     // [warp][8 rows][M_LD]
+  static constexpr int OFF_ML = OFF_M + WARPS * 8 * M_LD * 4;   // [warp][8 rows] (m, l)
+  static constexpr int OFF_ROW = OFF_ML + WARPS * 8 * 8;        // [ROWS] (C, limit)
+  static constexpr int OFF_BAR = OFF_ROW + ROWS * 8;
+  static constexpr int SMEM = OFF_BAR + NS * 16 + NS * 4 + 64;
+  static_assert(SMEM * CTAS_PER_SM + CTAS_PER_SM * 1024 <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory");
+};
+constexpr int kKv4PartRows = 32;                        // rows of a partial (the largest layout's)
+constexpr int kKv4PartFloats = kKv4PartRows * (kKv4D + 2);
+
+// E2M1 pairs of a word's four bytes -> half2 each (low half: low nibble).
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t* h) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// D += A B, 16x8x16, fp16 operands, FP32 accumulators.
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8x8 matrix of 16-bit elements over the warp (thread i: row i / 4, columns 2 (i % 4) ..).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return pack2<__half>(lo, hi); }
+
+// The power of two that brings a row with largest magnitude `amax` to [2^10, 2^11) (1 for a row
+// of zeros, infinities or NaN), and its inverse. bf16 rows need it to become fp16; fp16 rows keep 1.
+template <typename T>
+__device__ __forceinline__ float2 kv4_row_factor(float amax) {
+  if (!std::is_same<T, __nv_bfloat16>::value || !(amax > 0.f) || amax > 3.4e38f) return make_float2(1.f, 1.f);
+  int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 10;
+  e = max(-126, min(126, e));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(127 - e) << 23),
+                     __uint_as_float(static_cast<uint32_t>(127 + e) << 23));
+}
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(Kv4SplitLayout<NT>::THREADS, Kv4SplitLayout<NT>::CTAS_PER_SM)
+kv4_split_kernel(Kv4AttnArgs a) {
+  using L = Kv4SplitLayout<NT>;
+  extern __shared__ __align__(128) unsigned char kv4_smem[];
+  unsigned char* sm = kv4_smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
+  uint64_t* empty = full + L::NS;
+  volatile int* page_ok = reinterpret_cast<volatile int*>(empty + L::NS);
+  int* misc = const_cast<int*>(page_ok) + L::NS;        // scan: [0..8] warp sums, [9] total, [10..12] start
+  volatile int* abort_flag = misc + 15;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.Hq / a.c.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::NS; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, 2); }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // ---- this CTA's range of units ----
+  auto weight = [&](int s) -> int {
+    if (s >= a.S) return 0;
+    const Kv4Seq q = kv4_seq(a, s, blockIdx.x == 0);
+    return (q.n > 0 && q.n * group <= a.rows_max) ? ((q.ctx + 63) >> 6) * a.c.Hkv : 0;
+  };
+  int w0 = 0, total = 0, excl = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    // pass 0: the total; pass 1 (the same sums again): the sequence that holds the first unit
+    int run = 0, first = 0;
+    if (pass == 1) {
+      const int per = max(4, (total + gridDim.x - 1) / static_cast<int>(gridDim.x));
+      first = min(static_cast<int64_t>(per) * blockIdx.x, static_cast<int64_t>(total));
+      if (tid == 0) {
+        misc[10] = a.S; misc[11] = 0; misc[12] = min(per, total - first);
+        if (blockIdx.x == 0) a.plan[0] = per;
+      }
+      __syncthreads();
+    }
+    for (int s0 = 0; s0 < a.S; s0 += L::THREADS) {
+      if (pass == 0 || a.S > L::THREADS) {               // one chunk: kept from pass 0
+        w0 = weight(s0 + tid);
+        int x = w0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) misc[warp] = x;
+        __syncthreads();
+        excl = x - w0;
+        int sum = 0;
+        for (int i = 0; i <= L::WARPS; ++i) {
+          if (i < warp) excl += misc[i];
+          sum += misc[i];
+        }
+        if (pass == 0) total += sum;
+        else { excl += run; run += sum; }
+      }
+      if (pass == 1 && s0 + tid < a.S) {
+        if (blockIdx.x == 0) a.plan[1 + s0 + tid] = excl;
+        if (w0 > 0 && first >= excl && first < excl + w0) { misc[10] = s0 + tid; misc[11] = first - excl; }
+      }
+    }
+  }
+  __syncthreads();
+  Kv4Walk walk;
+  walk.s = misc[10];
+  walk.left = misc[12];
+  walk.h = walk.p = 0;
+  if (walk.s < a.S) {
+    const int np = (a.lens[walk.s] + 63) >> 6;
+    walk.h = misc[11] / np;
+    walk.p = misc[11] % np;
+  }
+  Kv4Seg g;
+  int gi = 0;                                           // units of this CTA so far
+
+  if (warp == L::WARPS) {
+    // ================================ producer ================================
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      int id = -1;
+      for (int p = g.p0; p < g.p1 && ok; ++p, ++gi) {
+        const int k = (p - g.p0) & 31;
+        if (k == 0) id = p + lane < g.p1 ? a.table[static_cast<int64_t>(g.s) * a.max_pages + p + lane] : -1;
+        const int page = __shfl_sync(0xffffffffu, id, k);
+        const int st = gi % L::NS;
+        if (gi >= L::NS && !bounded_wait_warp(empty + st, (gi / L::NS - 1) & 1, abort_flag,
+                                              wait_site(kKernelKv4Split, kRoleProducer, st, gi))) {
+          ok = false;
+          break;
+        }
+        const bool good = page >= 0 && page < a.c.num_pages;
+        if (lane == 0) {
+          page_ok[st] = good;
+          if (good) mbar_arrive_expect_tx(full + st, L::STAGE);
+          else { flag_error(kStatusBounds); mbar_arrive(full + st); }
+        }
+        __syncwarp();
+        if (good && lane < 4) {
+          const int64_t head = static_cast<int64_t>(page) * a.c.Hkv + g.h;
+          unsigned char* d = sm + st * L::STAGE;
+          if (lane == 0) bulk_load(d, a.c.k_pages + head * 4096, 4096, full + st);
+          else if (lane == 1) bulk_load(d + L::OFF_V, a.c.v_pages + head * 4096, 4096, full + st);
+          else if (lane == 2) bulk_load(d + L::OFF_KS, a.c.k_scales + head * 512, 512, full + st);
+          else bulk_load(d + L::OFF_VS, a.c.v_scales + head * 512, 512, full + st);
+        }
+        __syncwarp();
+      }
+    }
+    // never leave a copy in flight into this CTA's shared memory
+    for (int st = 0; st < L::NS && st < gi; ++st)
+      mbar_wait(full + st, ((gi - 1 - st) / L::NS) & 1);
+    return;
+  }
+
+  // ================================ attention ================================
+  const int c = lane >> 2, t = lane & 3;
+  const int pair = warp >> 1, half = warp & 1;
+  const float* row_c = reinterpret_cast<const float*>(sm + L::OFF_ROW);
+  const int* row_lim = reinterpret_cast<const int*>(sm + L::OFF_ROW) + L::ROWS;
+  while (walk.next(a, g)) {
+    const int rows = g.q.n * group;
+    // ---- Q: rows to fp16, zeros past the last; constants of each row ----
+    named_bar_sync(1, L::WARPS * 32);                   // the last segment's rows are done with
+    for (int r = warp; r < L::ROWS; r += L::WARPS) {
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < rows) {
+        const T* src = static_cast<const T*>(a.q) + (g.q.q0 + r / group) * a.q_stride +
+                       (g.h * group + r % group) * kKv4D + lane * 4;
+        const uint2 u = *reinterpret_cast<const uint2*>(src);
+        const float2 x = to_float2<T>(u.x), y = to_float2<T>(u.y);
+        f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+      }
+      float m = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float2 fac = kv4_row_factor<T>(m);
+      *reinterpret_cast<uint2*>(sm + L::OFF_Q + r * L::Q_LD + lane * 8) =
+          make_uint2(pack_half2(f[0] * fac.x, f[1] * fac.x), pack_half2(f[2] * fac.x, f[3] * fac.x));
+      if (lane == 0) {
+        const_cast<float*>(row_c)[r] = fac.y * (*a.c.k_ts * a.softmax_scale * kLog2e);
+        const_cast<int*>(row_lim)[r] = r < rows ? g.q.ctx - g.q.n + r / group : -1;
+      }
+    }
+    named_bar_sync(1, L::WARPS * 32);
+    const int lim_min = g.q.ctx - g.q.n;                 // keys every row sees
+    uint32_t q[NT <= 2 ? NT : 1][16];
+    auto load_q = [&](int nt, uint32_t* dst) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint4*>(dst)[k] =
+            *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + k * 16);
+    };
+    if constexpr (NT <= 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) load_q(nt, q[nt]);
+    }
+    float C[NT][2], m[NT][2], l[NT][2], o[NT][8][4];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        C[nt][k] = row_c[nt * 8 + 2 * t + k];
+        lim[nt][k] = row_lim[nt * 8 + 2 * t + k];
+        m[nt][k] = -INFINITY;
+        l[nt][k] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+
+    for (int p = g.p0; p < g.p1; ++p, ++gi) {
+      if ((gi & 3) != pair) continue;
+      const int st = gi % L::NS;
+      const bool there = bounded_wait_warp(full + st, (gi / L::NS) & 1, abort_flag,
+                                           wait_site(kKernelKv4Split, kRoleSoftmax, st, gi));
+      const int base = p * 64 + half * 32;               // the warp's first token
+      if (there && page_ok[st] && base < g.q.ctx) {
+        const unsigned char* sp = sm + st * L::STAGE;
+        // ---- S^T = K Q^T: two tiles of 16 tokens ----
+        float s[2][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+          const int tok = half * 32 + mt * 16 + c;
+          const uint4 ka = *reinterpret_cast<const uint4*>(sp + tok * 64 + t * 16);
+          const uint4 kb = *reinterpret_cast<const uint4*>(sp + (tok + 8) * 64 + t * 16);
+          const __half2 sa = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sp + L::OFF_KS + tok * 8 + t * 2));
+          const __half2 sb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sp + L::OFF_KS + (tok + 8) * 8 + t * 2));
+          const uint32_t* kaw = reinterpret_cast<const uint32_t*>(&ka);
+          const uint32_t* kbw = reinterpret_cast<const uint32_t*>(&kb);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {                  // a word: 8 channels, two k-steps' halves
+            const __half2 fa = w < 2 ? __low2half2(sa) : __high2half2(sa);
+            const __half2 fb = w < 2 ? __low2half2(sb) : __high2half2(sb);
+            uint32_t ha[4], hb[4];
+            e2m1x8_to_half2(kaw[w], ha);
+            e2m1x8_to_half2(kbw[w], hb);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { ha[k] = hmul2(ha[k], fa); hb[k] = hmul2(hb[k], fb); }
+            const uint32_t a0[4] = {ha[0], hb[0], ha[1], hb[1]}, a1[4] = {ha[2], hb[2], ha[3], hb[3]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (NT <= 2) {
+                mma16816(s[mt][nt], a0, q[nt][4 * w], q[nt][4 * w + 1]);
+                mma16816(s[mt][nt], a1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
+              } else {
+                const uint4 qq = *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + w * 16);
+                mma16816(s[mt][nt], a0, qq.x, qq.y);
+                mma16816(s[mt][nt], a1, qq.z, qq.w);
+              }
+            }
+          }
+        }
+        // ---- softmax: this thread's rows are 2 t, 2 t + 1 of each tile, its tokens c + 8 j ----
+        uint32_t pb[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[2][4];                                 // [row][token c + 8 j]
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[0][j] = s[j >> 1][nt][(j & 1) * 2] * C[nt][0];
+            x[1][j] = s[j >> 1][nt][(j & 1) * 2 + 1] * C[nt][1];
+          }
+          if (base + 31 > lim_min) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (base + c + 8 * j > lim[nt][0]) x[0][j] = -INFINITY;
+              if (base + c + 8 * j > lim[nt][1]) x[1][j] = -INFINITY;
+            }
+          }
+          float alpha[2], bias[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float mx = fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m_new = fmaxf(m[nt][k], mx);
+            const float m_use = m_new == -INFINITY ? 0.f : m_new;
+            alpha[k] = ex2_approx(m[nt][k] - m_use);     // 0 before the first key
+            m[nt][k] = m_new;
+            bias[k] = kPShift - m_use;
+          }
+          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            l[nt][0] *= alpha[0];
+            l[nt][1] *= alpha[1];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[nt][i][0] *= alpha[0]; o[nt][i][1] *= alpha[1];
+              o[nt][i][2] *= alpha[0]; o[nt][i][3] *= alpha[1];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p0 = ex2_approx(x[0][j] + bias[0]), p1 = ex2_approx(x[1][j] + bias[1]);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pb[j >> 1][nt][j & 1] = transpose8x8(pack_half2(p0, p1));
+          }
+        }
+        // ---- O^T += V^T P^T: two steps of 16 tokens ----
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          const int r0 = half * 16 + kt * 8 + t;         // this thread's token pairs: r0, r0 + 4
+          const uint4 va = *reinterpret_cast<const uint4*>(sp + L::OFF_V + r0 * 128 + c * 16);
+          const uint4 vb = *reinterpret_cast<const uint4*>(sp + L::OFF_V + (r0 + 4) * 128 + c * 16);
+          uint32_t sca = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + r0 * 2);
+          uint32_t scb = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + (r0 + 4) * 2);
+          if (base + 32 > g.q.ctx) {                     // slots behind the context: weight 0, value 0
+            const int left = g.q.ctx - p * 64;           // valid slots of the page
+            if (2 * r0 >= left) sca = 0; else if (2 * r0 + 1 >= left) sca &= 0xFFu;
+            if (2 * r0 + 8 >= left) scb = 0; else if (2 * r0 + 9 >= left) scb &= 0xFFu;
+          }
+          const __half2 fa = e4m3x2_to_half2(sca), fb = e4m3x2_to_half2(scb);
+          const uint32_t* vaw = reinterpret_cast<const uint32_t*>(&va);
+          const uint32_t* vbw = reinterpret_cast<const uint32_t*>(&vb);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t ha[4], hb[4];
+            e2m1x8_to_half2(vaw[w], ha);
+            e2m1x8_to_half2(vbw[w], hb);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { ha[k] = hmul2(ha[k], fa); hb[k] = hmul2(hb[k], fb); }
+            const uint32_t a0[4] = {ha[0], ha[1], hb[0], hb[1]}, a1[4] = {ha[2], ha[3], hb[2], hb[3]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(o[nt][2 * w], a0, pb[kt][nt][0], pb[kt][nt][1]);
+              mma16816(o[nt][2 * w + 1], a1, pb[kt][nt][0], pb[kt][nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st);
+    }
+
+    // ---- the eight warps' results joined, eight rows at a time ----
+    const bool whole = g.p0 == 0 && g.p1 == g.np;
+    float* mbuf = reinterpret_cast<float*>(sm + L::OFF_M);
+    float2* mlbuf = reinterpret_cast<float2*>(sm + L::OFF_ML);
+    float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (g.p0 > 0 ? 0 : 1)) * kKv4PartFloats;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) named_bar_sync(1, L::WARPS * 32);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float ls = l[nt][k];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 4);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 8);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+        if (c == 0) mlbuf[warp * 8 + 2 * t + k] = make_float2(m[nt][k], ls);
+        float* dst = mbuf + (warp * 8 + 2 * t + k) * L::M_LD + c * 16;   // channels 16 c + 2 i, + 1
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[nt][i][k], o[nt][i][2 + k], o[nt][i + 1][k], o[nt][i + 1][2 + k]);
+      }
+      named_bar_sync(1, L::WARPS * 32);
+      const int r = nt * 8 + warp;                       // a warp joins one row, a lane four channels
+      if (r < rows) {
+        float M = -INFINITY, ls = 0.f;
+#pragma unroll
+        for (int k = 0; k < L::WARPS; ++k) M = fmaxf(M, mlbuf[k * 8 + warp].x);
+        const float mu = M == -INFINITY ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < L::WARPS; ++k) {
+          const float2 ml = mlbuf[k * 8 + warp];
+          const float wgt = ex2_approx(ml.x - mu);
+          const float4 v = *reinterpret_cast<const float4*>(mbuf + (k * 8 + warp) * L::M_LD + lane * 4);
+          ls += wgt * ml.y;
+          acc.x += wgt * v.x; acc.y += wgt * v.y; acc.z += wgt * v.z; acc.w += wgt * v.w;
+        }
+        if (whole) {
+          const float f = ls == 0.f ? 0.f : *a.c.v_ts / ls;
+          const int64_t orow = static_cast<int64_t>(g.q.q0 + r / group) * a.Hq + g.h * group + r % group;
+          *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * kKv4D + lane * 4) =
+              make_uint2(pack2<T>(acc.x * f, acc.y * f), pack2<T>(acc.z * f, acc.w * f));
+          if (a.lse != nullptr && lane == 0)
+            a.lse[orow] = ls == 0.f ? -INFINITY : (M + log2f(ls) - kPShift) * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(part + r * kKv4D + lane * 4) = acc;
+          if (lane == 0) *reinterpret_cast<float2*>(part + kKv4PartRows * kKv4D + 2 * r) = make_float2(M, ls);
+        }
+      }
+    }
+  }
+}
+
+// Joins the partials of the pairs that cross CTAs. One CTA per (sequence, KV head) and row; a thread
+// per channel.
+template <typename T>
+__global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4AttnArgs a) {
+  const int s = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv, r = blockIdx.y;
+  const int group = a.Hq / a.c.Hkv;
+  const Kv4Seq q = kv4_seq(a, s, false);
+  if (q.n <= 0 || q.n * group > a.rows_max || r >= q.n * group) return;
+  const int per = a.plan[0], np = (q.ctx + 63) >> 6;
+  const int first = a.plan[1 + s] + h * np;
+  const int c0 = first / per, c1 = (first + np - 1) / per;
+  if (c0 == c1) return;                                 // written by the split kernel
+  const int tid = threadIdx.x;
+  auto part = [&](int cta) {
+    return a.part + static_cast<int64_t>(2 * cta + (cta == c0 ? 1 : 0)) * kKv4PartFloats;
+  };
+  float M = -INFINITY;
+  for (int k = c0 + (tid & 31); k <= c1; k += 32) M = fmaxf(M, part(k)[kKv4PartRows * kKv4D + 2 * r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float mu = M == -INFINITY ? 0.f : M;
+  float acc = 0.f, ls = 0.f;
+#pragma unroll 4
+  for (int k = c0; k <= c1; ++k) {
+    const float* p = part(k);
+    const float2 ml = *reinterpret_cast<const float2*>(p + kKv4PartRows * kKv4D + 2 * r);
+    const float w = ex2_approx(ml.x - mu);
+    ls += w * ml.y;
+    acc += w * p[r * kKv4D + tid];
+  }
+  const int64_t orow = static_cast<int64_t>(q.q0 + r / group) * a.Hq + h * group + r % group;
+  const float f = ls == 0.f ? 0.f : *a.c.v_ts / ls;
+  static_cast<T*>(a.out)[orow * kKv4D + tid] = static_cast<T>(acc * f);
+  if (a.lse != nullptr && tid == 0) a.lse[orow] = ls == 0.f ? -INFINITY : (M + log2f(ls) - kPShift) * kLn2;
+}
+
+}  // namespace qk4v8

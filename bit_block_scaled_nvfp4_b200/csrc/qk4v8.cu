@@ -14,6 +14,7 @@
 #include "decode.cuh"
 #include "append.cuh"
 #include "kv4.cuh"
+#include "kv4_split.cuh"
 #include "pages.cuh"
 
 using namespace qk4v8;
@@ -120,6 +121,7 @@ size_t qk4v8_struct_size(int32_t which) {
          : which == 3 ? sizeof(qk4v8_qkv_params)
          : which == 4 ? sizeof(qk4v8_kv4_cache)
          : which == 5 ? sizeof(qk4v8_kv4_tokens)
+         : which == 6 ? sizeof(qk4v8_kv4_attn_params)
                       : 0;
 }
 
@@ -845,6 +847,96 @@ extern "C" qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* p, cudaStream_t s
   else if (p->dtype == QK4V8_F16) kv4_read_kernel<__half><<<grid, 256, 0, stream>>>(a);
   else kv4_read_kernel<float><<<grid, 256, 0, stream>>>(a);
   return launch_status();
+}
+
+// ------------------------------------------------------------------------------------------
+// Attention over the 4-bit cache (kv4_split.cuh)
+// ------------------------------------------------------------------------------------------
+namespace {
+struct Kv4Schedule {
+  int nt;                 // split kernel: tiles of eight rows
+  int rows_max;           // sequences with at most this many rows a KV head go to it
+  int split_ctas;
+  size_t part_off, bytes; // workspace: plan, then the partials
+};
+// nt 1, 2 or 4: rows a KV head reads at once. Where every sequence has at most 32 rows the split
+// kernel takes them all; otherwise it takes the sequences of one token.
+Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
+  Kv4Schedule s;
+  const int64_t group = p->q_heads / p->cache.kv_heads, rows = p->max_q * group;
+  const int64_t r = rows <= 32 ? rows : group;
+  s.nt = r <= 8 ? 1 : r <= 16 ? 2 : 4;
+  s.rows_max = 8 * s.nt;
+  const int64_t units = static_cast<int64_t>(p->num_seqs) * ((p->max_context + 63) / 64) * p->cache.kv_heads;
+  const int64_t ctas = static_cast<int64_t>(sm_count()) * (s.nt == 1 ? 2 : 1);
+  s.split_ctas = static_cast<int>(ctas < (units + 3) / 4 ? ctas : (units + 3) / 4);
+  s.part_off = (4 * (static_cast<size_t>(p->num_seqs) + 1) + 15) / 16 * 16;
+  s.bytes = s.part_off + static_cast<size_t>(s.split_ctas) * 2 * kKv4PartFloats * 4;
+  return s;
+}
+
+qk4v8_status check_kv4_attn(const qk4v8_kv4_attn_params* p) {
+  if (p == nullptr || !p->q || !p->context_lens || !p->page_table || !p->out) return QK4V8_ERR_INVALID_ARG;
+  if (const qk4v8_status st = check_kv4_cache(p->cache); st != QK4V8_OK) return st;
+  if (p->dtype != QK4V8_F16 && p->dtype != QK4V8_BF16) return QK4V8_ERR_INVALID_ARG;
+  if (p->total_q < 0 || p->num_seqs <= 0 || p->max_pages <= 0 || p->q_heads <= 0 || p->max_q <= 0 ||
+      p->max_context <= 0 || p->q_heads % p->cache.kv_heads)
+    return QK4V8_ERR_INVALID_ARG;
+  if (p->cu_q == nullptr && (p->total_q != p->num_seqs || p->max_q != 1)) return QK4V8_ERR_INVALID_ARG;
+  if (p->q_stride < static_cast<int64_t>(p->q_heads) * kKv4D || p->q_stride % 8) return QK4V8_ERR_INVALID_ARG;
+  if (!(p->softmax_scale > 0.f)) return QK4V8_ERR_INVALID_ARG;
+  if (!aligned(p->q, 16) || !aligned(p->out, 16) || !aligned(p->lse, 4)) return QK4V8_ERR_INVALID_ARG;
+  if (p->q_heads / p->cache.kv_heads > 16) return QK4V8_ERR_UNSUPPORTED;
+  if ((p->max_context - 1) / 64 >= p->max_pages) return QK4V8_ERR_INVALID_ARG;
+  // units of work (a page of a KV head of a sequence) are counted in 32 bits
+  const int64_t head_pages = static_cast<int64_t>((p->max_context - 1) / 64 + 1) * p->cache.kv_heads;
+  if (head_pages > 0x3fffffff / p->num_seqs) return QK4V8_ERR_UNSUPPORTED;
+  return QK4V8_OK;
+}
+
+template <int NT, typename T>
+qk4v8_status launch_kv4_split(const Kv4AttnArgs& a, int ctas, cudaStream_t stream) {
+  using L = Kv4SplitLayout<NT>;
+  static PerDeviceOnce opt_in;
+  if (!opt_in.run(current_device(), [] { return set_smem(kv4_split_kernel<NT, T>, L::SMEM); })) return QK4V8_ERR_CUDA;
+  kv4_split_kernel<NT, T><<<ctas, L::THREADS, L::SMEM, stream>>>(a);
+  return launch_status();
+}
+
+template <typename T>
+qk4v8_status launch_kv4_attn(const qk4v8_kv4_attn_params* p, const Kv4Schedule& sc, const Kv4AttnArgs& a,
+                             cudaStream_t stream) {
+  const qk4v8_status st = sc.nt == 1   ? launch_kv4_split<1, T>(a, sc.split_ctas, stream)
+                          : sc.nt == 2 ? launch_kv4_split<2, T>(a, sc.split_ctas, stream)
+                                       : launch_kv4_split<4, T>(a, sc.split_ctas, stream);
+  if (st != QK4V8_OK) return st;
+  const dim3 grid(static_cast<unsigned>(p->num_seqs * p->cache.kv_heads), static_cast<unsigned>(sc.rows_max));
+  kv4_merge_kernel<T><<<grid, 128, 0, stream>>>(a);
+  return launch_status();
+}
+}  // namespace
+
+extern "C" size_t attn_kv4_paged_workspace_size(const qk4v8_kv4_attn_params* p) {
+  return check_kv4_attn(p) == QK4V8_OK ? kv4_schedule(p).bytes : 0;
+}
+
+extern "C" qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* p, void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream) {
+  if (const qk4v8_status st = check_kv4_attn(p); st != QK4V8_OK) return st;
+  if (p->total_q == 0) return QK4V8_OK;
+  const Kv4Schedule sc = kv4_schedule(p);
+  if (static_cast<int64_t>(p->max_q) * (p->q_heads / p->cache.kv_heads) > 32) return QK4V8_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < sc.bytes) return QK4V8_ERR_INVALID_ARG;
+  Kv4AttnArgs a;
+  a.c = kv4_cache(p->cache);
+  a.q = p->q; a.q_stride = p->q_stride; a.cu_q = p->cu_q; a.lens = p->context_lens; a.table = p->page_table;
+  a.total_q = p->total_q; a.S = p->num_seqs; a.max_pages = p->max_pages; a.Hq = p->q_heads; a.max_q = p->max_q;
+  a.max_context = p->max_context; a.rows_max = sc.rows_max; a.softmax_scale = p->softmax_scale;
+  a.out = p->out; a.lse = p->lse;
+  a.plan = static_cast<int32_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + sc.part_off);
+  return p->dtype == QK4V8_BF16 ? launch_kv4_attn<__nv_bfloat16>(p, sc, a, stream)
+                                : launch_kv4_attn<__half>(p, sc, a, stream);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -49,7 +49,7 @@ int qk4v8_version(void);
 /* sizeof the parameter structs, for bindings that mirror them: which = 0 gives
  * sizeof(qk4v8_fwd_params), 1 sizeof(qk4v8_decode_params), 2 sizeof(qk4v8_append_params),
  * 3 sizeof(qk4v8_qkv_params), 4 sizeof(qk4v8_kv4_cache), 5 sizeof(qk4v8_kv4_tokens),
- * anything else 0. */
+ * 6 sizeof(qk4v8_kv4_attn_params), anything else 0. */
 size_t qk4v8_struct_size(int32_t which);
 
 /* Human-readable name of a status code (static string). */
@@ -456,6 +456,44 @@ typedef struct {
 
 qk4v8_status kv4_append_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream);
 qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream);
+
+/*
+ * attn_kv4_paged — causal attention of packed 16-bit queries over the 4-bit cache, from one
+ * token a sequence (a decoding step) to whole prompts, sequences of any lengths in one call:
+ *   O_i = sum_j softmax_j(softmax_scale q_i . k_j) v_j,  j <= context_lens[s] - n_s + i,
+ * for the n_s = cu_q[s+1] - cu_q[s] query tokens of sequence s, the last n_s of its context
+ * (append them first). Query head h reads KV head h / (q_heads / kv_heads). Neither the queries
+ * nor the weights are quantized: q keeps its 16 bits, K and V their cached values, scores,
+ * running maxima and sums are FP32, and the weights enter P V as fp16 scaled by 2^6.
+ * Rows at or past cu_q[S] of out (and lse) are left as they were.
+ * Device checks, each setting QK4V8_ERR_BOUNDS: n_s outside [0, max_q], cu_q[s] or cu_q[s+1]
+ * outside [0, total_q], or a context outside [n_s, min(max_context, 64 * max_pages)] (the
+ * sequence's rows are left as they were); a page id outside [0, num_pages) (that page's keys
+ * are left out; a row with no key left gets O = 0 and lse = -inf).
+ * workspace  >= attn_kv4_paged_workspace_size(params) bytes, 16-byte aligned; its contents
+ *            before and after mean nothing, calls that may overlap need one each.
+ */
+typedef struct {
+  qk4v8_kv4_cache cache;
+  const void* q;               /* [total_q, Hq, D], heads and channels contiguous, 16-byte aligned */
+  int64_t q_stride;            /* elements from one token to the next (>= Hq * D, % 8 == 0) */
+  qk4v8_dtype dtype;           /* of q and out: F16 or BF16 */
+  int32_t total_q;
+  const int32_t* cu_q;         /* [S + 1]; or NULL: one token a sequence (total_q == S) */
+  const int32_t* context_lens; /* [S], query tokens included */
+  const int32_t* page_table;   /* [S, max_pages] */
+  int32_t num_seqs, max_pages;
+  int32_t q_heads;             /* a multiple of kv_heads, at most 16 times it */
+  int32_t max_q;               /* host-side bound on n_s */
+  int32_t max_context;         /* host-side bound on context_lens */
+  float softmax_scale;
+  void* out;                   /* [total_q, Hq, D] contiguous, 16-byte aligned */
+  float* lse;                  /* optional [total_q, Hq] natural-log sum-exp; or NULL */
+} qk4v8_kv4_attn_params;
+
+size_t attn_kv4_paged_workspace_size(const qk4v8_kv4_attn_params* params);
+qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* params, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Page pool: which pages of a cache (of either kind; all layers of a model share one page table)

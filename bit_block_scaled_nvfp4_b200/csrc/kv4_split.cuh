@@ -24,10 +24,13 @@
 // them; through shared or tensor memory every decoded byte would be written and read again.
 //
 // Work split: the pages of all (sequence, KV head) pairs form one line, cut into equal
-// consecutive ranges, one a CTA, whatever the lengths. A CTA's eight warps take half a page each
-// (four pages at a time), each with its own running maximum, and are merged through shared memory
-// where a pair ends. A pair inside one CTA is written out; one that crosses CTAs leaves
-// partials (O, m, l) that the merge kernel joins. A ninth warp brings pages in by bulk copies.
+// consecutive ranges, one a CTA and one CTA an SM, whatever the lengths. The CTA's warps take
+// pages in turn, each with its own running maximum, and are joined through shared memory where a
+// pair ends. A pair inside one CTA is written out; one that crosses CTAs leaves partials
+// (O, m, l) that the merge kernel joins. Each warp loads its own pages, two stages of one page,
+// by 16-byte asynchronous copies, with no barrier between warps until a pair ends. (One warp
+// issuing bulk copies for all of them reached 1 page in 1020 cycles, 4 copies of 4096 + 4096 +
+// 512 + 512 bytes: 33 % of the HBM rate.)
 #pragma once
 #include <type_traits>
 #include "kv4.cuh"
@@ -52,7 +55,6 @@ struct Kv4AttnArgs {
 };
 
 constexpr float kPShift = 6.f;
-constexpr uint32_t kKernelKv4Split = 4;
 
 struct Kv4Seq {
   int q0, n, ctx;            // first query row, query tokens, context
@@ -72,51 +74,70 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool flag
   return q;
 }
 
-// One (sequence, KV head) pair's part of a CTA's range: pages [p0, p1) of np.
-struct Kv4Seg {
-  int s, h, p0, p1, np;
-  Kv4Seq q;
-};
-// Walks a CTA's range of units (a unit: one page of one KV head), sequence by sequence, head by head.
+// A position in the line of units (a unit: one page of one KV head of a sequence; sequence by
+// sequence, head by head), and the units left from there in the CTA's range.
 struct Kv4Walk {
-  int s, h, p, left;         // next unit, units left
-  __device__ __forceinline__ bool next(const Kv4AttnArgs& a, Kv4Seg& g) {
-    if (left <= 0) return false;
+  int s, h, p, np, left;
+  Kv4Seq q;
+  // the first sequence from s on that the split kernel takes
+  __device__ __forceinline__ void find(const Kv4AttnArgs& a) {
     const int group = a.Hq / a.c.Hkv;
-    for (;; ++s) {
-      if (s >= a.S) return false;
-      g.q = kv4_seq(a, s, false);
-      if (g.q.n > 0 && g.q.n * group <= a.rows_max) break;
+    for (; s < a.S; ++s) {
+      q = kv4_seq(a, s, false);
+      if (q.n > 0 && q.n * group <= a.rows_max) {
+        np = (q.ctx + 63) >> 6;
+        return;
+      }
     }
-    g.s = s; g.h = h; g.p0 = p;
-    g.np = (g.q.ctx + 63) >> 6;
-    g.p1 = min(g.np, p + left);
-    left -= g.p1 - p;
-    p = 0;
-    if (++h == a.c.Hkv) { h = 0; ++s; }
-    return true;
+    left = 0;
+  }
+  __device__ __forceinline__ void next_pair(const Kv4AttnArgs& a) {
+    if (++h == a.c.Hkv) {
+      h = 0;
+      ++s;
+      find(a);
+    }
+  }
+  __device__ __forceinline__ void advance(const Kv4AttnArgs& a, int units) {
+    p += units;
+    left -= units;
+    while (left > 0 && p >= np) {
+      p -= np;
+      next_pair(a);
+    }
   }
 };
 
 template <int NT>
 struct Kv4SplitLayout {
-  static constexpr int WARPS = 8, THREADS = WARPS * 32 + 32;
-  static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
-  static constexpr int NS = NT == 1 ? 8 : 16;           // ring stages of one page
+  static constexpr int WARPS = NT == 4 ? 8 : 12, THREADS = WARPS * 32;
+  static constexpr int NS = 2;                          // stages a warp, of one page
+  static constexpr int MT = NT == 1 ? 4 : 2;            // tiles of 16 tokens taken at once
   static constexpr int ROWS = NT * 8;
   static constexpr int STAGE = 9216, OFF_V = 4096, OFF_KS = 8192, OFF_VS = 8704;
   static constexpr int Q_LD = 272;                      // bytes of a Q row (256 + 16)
-  static constexpr int M_LD = 132;                      // floats of a merge row (128 + 4)
-  static constexpr int OFF_Q = NS * STAGE;
-  static constexpr int OFF_M = OFF_Q + ROWS * Q_LD;     // [warp][8 rows][M_LD]
-  static constexpr int OFF_ML = OFF_M + WARPS * 8 * M_LD * 4;   // [warp][8 rows] (m, l)
-  static constexpr int OFF_ROW = OFF_ML + WARPS * 8 * 8;        // [ROWS] (C, limit)
-  static constexpr int OFF_BAR = OFF_ROW + ROWS * 8;
-  static constexpr int SMEM = OFF_BAR + NS * 16 + NS * 4 + 64;
-  static_assert(SMEM * CTAS_PER_SM + CTAS_PER_SM * 1024 <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory");
+  static constexpr int M_LD = 132;                      // floats of a row in the join (128 + 4)
+  static constexpr int OFF_Q = WARPS * NS * STAGE;
+  static constexpr int OFF_ML = OFF_Q + ROWS * Q_LD;    // [warp][8 rows] (m, l)
+  static constexpr int OFF_ROW = OFF_ML + WARPS * 8 * 8;        // [ROWS] C, then [ROWS] limit
+  static constexpr int OFF_MISC = OFF_ROW + ROWS * 8;   // [12] warp sums, [3] start of the range
+  static constexpr int OFF_AT = OFF_MISC + 64;          // [warp] where its O lies in the join
+  static constexpr int SMEM = OFF_AT + WARPS * 4;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(8 * M_LD * 4 <= STAGE, "a stage holds a warp's O of eight rows");
 };
 constexpr int kKv4PartRows = 32;                        // rows of a partial (the largest layout's)
 constexpr int kKv4PartFloats = kKv4PartRows * (kKv4D + 2);
+
+// 16-byte asynchronous copy past L1.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // E2M1 pairs of a word's four bytes -> half2 each (low half: low nibble).
 __device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t* h) {
@@ -156,24 +177,15 @@ __device__ __forceinline__ float2 kv4_row_factor(float amax) {
 }
 
 template <int NT, typename T>
-__global__ void __launch_bounds__(Kv4SplitLayout<NT>::THREADS, Kv4SplitLayout<NT>::CTAS_PER_SM)
+__global__ void __launch_bounds__(Kv4SplitLayout<NT>::THREADS, 1)
 kv4_split_kernel(Kv4AttnArgs a) {
   using L = Kv4SplitLayout<NT>;
   extern __shared__ __align__(128) unsigned char kv4_smem[];
   unsigned char* sm = kv4_smem;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
-  uint64_t* empty = full + L::NS;
-  volatile int* page_ok = reinterpret_cast<volatile int*>(empty + L::NS);
-  int* misc = const_cast<int*>(page_ok) + L::NS;        // scan: [0..8] warp sums, [9] total, [10..12] start
-  volatile int* abort_flag = misc + 15;
+  int* misc = reinterpret_cast<int*>(sm + L::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.Hq / a.c.Hkv;
 
-  if (tid == 0) {
-    for (int i = 0; i < L::NS; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, 2); }
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
   // ---- this CTA's range of units ----
   auto weight = [&](int s) -> int {
     if (s >= a.S) return 0;
@@ -188,7 +200,7 @@ kv4_split_kernel(Kv4AttnArgs a) {
       const int per = max(4, (total + gridDim.x - 1) / static_cast<int>(gridDim.x));
       first = min(static_cast<int64_t>(per) * blockIdx.x, static_cast<int64_t>(total));
       if (tid == 0) {
-        misc[10] = a.S; misc[11] = 0; misc[12] = min(per, total - first);
+        misc[12] = a.S; misc[13] = 0; misc[14] = min(per, total - first);
         if (blockIdx.x == 0) a.plan[0] = per;
       }
       __syncthreads();
@@ -207,7 +219,7 @@ kv4_split_kernel(Kv4AttnArgs a) {
         __syncthreads();
         excl = x - w0;
         int sum = 0;
-        for (int i = 0; i <= L::WARPS; ++i) {
+        for (int i = 0; i < L::WARPS; ++i) {
           if (i < warp) excl += misc[i];
           sum += misc[i];
         }
@@ -216,71 +228,71 @@ kv4_split_kernel(Kv4AttnArgs a) {
       }
       if (pass == 1 && s0 + tid < a.S) {
         if (blockIdx.x == 0) a.plan[1 + s0 + tid] = excl;
-        if (w0 > 0 && first >= excl && first < excl + w0) { misc[10] = s0 + tid; misc[11] = first - excl; }
+        if (w0 > 0 && first >= excl && first < excl + w0) { misc[12] = s0 + tid; misc[13] = first - excl; }
       }
     }
   }
   __syncthreads();
-  Kv4Walk walk;
-  walk.s = misc[10];
-  walk.left = misc[12];
+  Kv4Walk walk;                                         // the pair at hand
+  walk.s = misc[12];
+  walk.left = misc[14];
   walk.h = walk.p = 0;
-  if (walk.s < a.S) {
-    const int np = (a.lens[walk.s] + 63) >> 6;
-    walk.h = misc[11] / np;
-    walk.p = misc[11] % np;
+  walk.find(a);
+  if (walk.left > 0) {
+    walk.h = misc[13] / walk.np;
+    walk.p = misc[13] % walk.np;
   }
-  Kv4Seg g;
-  int gi = 0;                                           // units of this CTA so far
-
-  if (warp == L::WARPS) {
-    // ================================ producer ================================
-    bool ok = true;
-    while (ok && walk.next(a, g)) {
-      int id = -1;
-      for (int p = g.p0; p < g.p1 && ok; ++p, ++gi) {
-        const int k = (p - g.p0) & 31;
-        if (k == 0) id = p + lane < g.p1 ? a.table[static_cast<int64_t>(g.s) * a.max_pages + p + lane] : -1;
-        const int page = __shfl_sync(0xffffffffu, id, k);
-        const int st = gi % L::NS;
-        if (gi >= L::NS && !bounded_wait_warp(empty + st, (gi / L::NS - 1) & 1, abort_flag,
-                                              wait_site(kKernelKv4Split, kRoleProducer, st, gi))) {
-          ok = false;
-          break;
-        }
-        const bool good = page >= 0 && page < a.c.num_pages;
-        if (lane == 0) {
-          page_ok[st] = good;
-          if (good) mbar_arrive_expect_tx(full + st, L::STAGE);
-          else { flag_error(kStatusBounds); mbar_arrive(full + st); }
-        }
-        __syncwarp();
-        if (good && lane < 4) {
-          const int64_t head = static_cast<int64_t>(page) * a.c.Hkv + g.h;
-          unsigned char* d = sm + st * L::STAGE;
-          if (lane == 0) bulk_load(d, a.c.k_pages + head * 4096, 4096, full + st);
-          else if (lane == 1) bulk_load(d + L::OFF_V, a.c.v_pages + head * 4096, 4096, full + st);
-          else if (lane == 2) bulk_load(d + L::OFF_KS, a.c.k_scales + head * 512, 512, full + st);
-          else bulk_load(d + L::OFF_VS, a.c.v_scales + head * 512, 512, full + st);
-        }
-        __syncwarp();
-      }
+  Kv4Walk ahead = walk;                                 // the next page this warp loads
+  ahead.advance(a, warp);
+  unsigned char* ring = sm + warp * (L::NS * L::STAGE);
+  auto page_of = [&](const Kv4Walk& w) {
+    return w.left > 0 ? a.table[static_cast<int64_t>(w.s) * a.max_pages + w.p] : -1;
+  };
+  // Starts the loads of a page into a stage and moves on; whether there was one.
+  auto load_page = [&](int st, int page) -> bool {
+    const bool mine = ahead.left > 0;
+    const bool good = mine && page >= 0 && page < a.c.num_pages;
+    if (good) {
+      const int64_t head = static_cast<int64_t>(page) * a.c.Hkv + ahead.h;
+      unsigned char* d = ring + st * L::STAGE + lane * 16;
+      const uint8_t* k = a.c.k_pages + head * 4096 + lane * 16;
+      const uint8_t* v = a.c.v_pages + head * 4096 + lane * 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cp_async16(d + i * 512, k + i * 512);
+      cp_async16(d + L::OFF_KS, a.c.k_scales + head * 512 + lane * 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cp_async16(d + L::OFF_V + i * 512, v + i * 512);
+      cp_async16(d + L::OFF_VS, a.c.v_scales + head * 512 + lane * 16);
+    } else if (mine && lane == 0) {
+      flag_error(kStatusBounds);
     }
-    // never leave a copy in flight into this CTA's shared memory
-    for (int st = 0; st < L::NS && st < gi; ++st)
-      mbar_wait(full + st, ((gi - 1 - st) / L::NS) & 1);
-    return;
-  }
+    cp_async_commit();
+    if (mine) ahead.advance(a, L::WARPS);
+    return good;
+  };
+  bool ok0 = load_page(0, page_of(ahead));              // stage `st` holds the warp's next page
+  bool ok1 = load_page(1, page_of(ahead));
+  int st = 0, gi = 0;                                   // gi: units of this CTA before the pair
 
   // ================================ attention ================================
+  constexpr int MT = L::MT;
   const int c = lane >> 2, t = lane & 3;
-  const int pair = warp >> 1, half = warp & 1;
-  const float* row_c = reinterpret_cast<const float*>(sm + L::OFF_ROW);
-  const int* row_lim = reinterpret_cast<const int*>(sm + L::OFF_ROW) + L::ROWS;
-  while (walk.next(a, g)) {
+  float* row_c = reinterpret_cast<float*>(sm + L::OFF_ROW);
+  int* row_lim = reinterpret_cast<int*>(sm + L::OFF_ROW) + L::ROWS;
+  bool owed = false;                                    // a stage to be loaded after the join
+  while (walk.left > 0) {
+    struct { Kv4Seq q; int h, p0, p1, np; } g = {walk.q, walk.h, walk.p, min(walk.np, walk.p + walk.left), walk.np};
+    walk.left -= g.p1 - g.p0;
+    walk.p = 0;
+    if (walk.left > 0) walk.next_pair(a);
     const int rows = g.q.n * group;
     // ---- Q: rows to fp16, zeros past the last; constants of each row ----
-    named_bar_sync(1, L::WARPS * 32);                   // the last segment's rows are done with
+    __syncthreads();                                    // the last pair's rows and join are done with
+    if (owed) {
+      const bool good = load_page(st ^ 1, page_of(ahead));
+      (st ? ok0 : ok1) = good;
+      owed = false;
+    }
     for (int r = warp; r < L::ROWS; r += L::WARPS) {
       float f[4] = {0.f, 0.f, 0.f, 0.f};
       if (r < rows) {
@@ -297,198 +309,211 @@ kv4_split_kernel(Kv4AttnArgs a) {
       *reinterpret_cast<uint2*>(sm + L::OFF_Q + r * L::Q_LD + lane * 8) =
           make_uint2(pack_half2(f[0] * fac.x, f[1] * fac.x), pack_half2(f[2] * fac.x, f[3] * fac.x));
       if (lane == 0) {
-        const_cast<float*>(row_c)[r] = fac.y * (*a.c.k_ts * a.softmax_scale * kLog2e);
-        const_cast<int*>(row_lim)[r] = r < rows ? g.q.ctx - g.q.n + r / group : -1;
+        row_c[r] = fac.y * (*a.c.k_ts * a.softmax_scale * kLog2e);
+        row_lim[r] = r < rows ? g.q.ctx - g.q.n + r / group : -1;
       }
     }
-    named_bar_sync(1, L::WARPS * 32);
-    const int lim_min = g.q.ctx - g.q.n;                 // keys every row sees
+    __syncthreads();
+    // a thread's rows of a tile: 2 t and 2 t + 1, in the halves of its pairs
     uint32_t q[NT <= 2 ? NT : 1][16];
-    auto load_q = [&](int nt, uint32_t* dst) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        reinterpret_cast<uint4*>(dst)[k] =
-            *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + k * 16);
-    };
     if constexpr (NT <= 2) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) load_q(nt, q[nt]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<uint4*>(q[nt])[k] =
+              *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + k * 16);
     }
-    float C[NT][2], m[NT][2], l[NT][2], o[NT][8][4];
-    int lim[NT][2];
+    float2 m[NT], l[NT];
+    float o[NT][8][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        C[nt][k] = row_c[nt * 8 + 2 * t + k];
-        lim[nt][k] = row_lim[nt * 8 + 2 * t + k];
-        m[nt][k] = -INFINITY;
-        l[nt][k] = 0.f;
-      }
+      m[nt] = make_float2(-INFINITY, -INFINITY);
+      l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-    for (int p = g.p0; p < g.p1; ++p, ++gi) {
-      if ((gi & 3) != pair) continue;
-      const int st = gi % L::NS;
-      const bool there = bounded_wait_warp(full + st, (gi / L::NS) & 1, abort_flag,
-                                           wait_site(kKernelKv4Split, kRoleSoftmax, st, gi));
-      const int base = p * 64 + half * 32;               // the warp's first token
-      if (there && page_ok[st] && base < g.q.ctx) {
-        const unsigned char* sp = sm + st * L::STAGE;
-        // ---- S^T = K Q^T: two tiles of 16 tokens ----
-        float s[2][NT][4];
+    for (int p = g.p0 + (warp + L::WARPS - gi % L::WARPS) % L::WARPS; p < g.p1; p += L::WARPS) {
+      const int next = page_of(ahead);
+      cp_async_wait<1>();
+      __syncwarp();
+      if (st ? ok1 : ok0) {
+        const unsigned char* sp = ring + st * L::STAGE;
+#pragma unroll 1
+        for (int first = 0; first < 64; first += MT * 16) {
+          // ---- S^T = K Q^T: MT tiles of 16 tokens ----
+          float s[MT][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
-          const int tok = half * 32 + mt * 16 + c;
-          const uint4 ka = *reinterpret_cast<const uint4*>(sp + tok * 64 + t * 16);
-          const uint4 kb = *reinterpret_cast<const uint4*>(sp + (tok + 8) * 64 + t * 16);
-          const __half2 sa = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sp + L::OFF_KS + tok * 8 + t * 2));
-          const __half2 sb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sp + L::OFF_KS + (tok + 8) * 8 + t * 2));
-          const uint32_t* kaw = reinterpret_cast<const uint32_t*>(&ka);
-          const uint32_t* kbw = reinterpret_cast<const uint32_t*>(&kb);
+            for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+            const int tok = first + mt * 16 + c;
+            const uint4 ka = *reinterpret_cast<const uint4*>(sp + tok * 64 + t * 16);
+            const uint4 kb = *reinterpret_cast<const uint4*>(sp + (tok + 8) * 64 + t * 16);
+            const __half2 sa = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sp + L::OFF_KS + tok * 8 + t * 2));
+            const __half2 sb = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sp + L::OFF_KS + (tok + 8) * 8 + t * 2));
+            const uint32_t* kaw = reinterpret_cast<const uint32_t*>(&ka);
+            const uint32_t* kbw = reinterpret_cast<const uint32_t*>(&kb);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {                  // a word: 8 channels, two k-steps' halves
-            const __half2 fa = w < 2 ? __low2half2(sa) : __high2half2(sa);
-            const __half2 fb = w < 2 ? __low2half2(sb) : __high2half2(sb);
-            uint32_t ha[4], hb[4];
-            e2m1x8_to_half2(kaw[w], ha);
-            e2m1x8_to_half2(kbw[w], hb);
+            for (int w = 0; w < 4; ++w) {                  // a word: 8 channels, two k-steps' halves
+              const __half2 fa = w < 2 ? __low2half2(sa) : __high2half2(sa);
+              const __half2 fb = w < 2 ? __low2half2(sb) : __high2half2(sb);
+              uint32_t ha[4], hb[4];
+              e2m1x8_to_half2(kaw[w], ha);
+              e2m1x8_to_half2(kbw[w], hb);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) { ha[k] = hmul2(ha[k], fa); hb[k] = hmul2(hb[k], fb); }
-            const uint32_t a0[4] = {ha[0], hb[0], ha[1], hb[1]}, a1[4] = {ha[2], hb[2], ha[3], hb[3]};
+              for (int k = 0; k < 4; ++k) { ha[k] = hmul2(ha[k], fa); hb[k] = hmul2(hb[k], fb); }
+              const uint32_t a0[4] = {ha[0], hb[0], ha[1], hb[1]}, a1[4] = {ha[2], hb[2], ha[3], hb[3]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (NT <= 2) {
-                mma16816(s[mt][nt], a0, q[nt][4 * w], q[nt][4 * w + 1]);
-                mma16816(s[mt][nt], a1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
-              } else {
-                const uint4 qq = *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + w * 16);
-                mma16816(s[mt][nt], a0, qq.x, qq.y);
-                mma16816(s[mt][nt], a1, qq.z, qq.w);
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (NT <= 2) {
+                  mma16816(s[mt][nt], a0, q[nt][4 * w], q[nt][4 * w + 1]);
+                  mma16816(s[mt][nt], a1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
+                } else {
+                  const uint4 qq = *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + w * 16);
+                  mma16816(s[mt][nt], a0, qq.x, qq.y);
+                  mma16816(s[mt][nt], a1, qq.z, qq.w);
+                }
+              }
+            }
+          }
+          // ---- softmax over the MT * 16 tokens; this thread has tokens c + 8 j ----
+          uint32_t pb[MT][NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + 2 * t;
+            if (p * 64 + 63 > g.q.ctx - g.q.n) {            // keys that not every row sees
+              const int lim0 = row_lim[r] - p * 64 - first - c, lim1 = row_lim[r + 1] - p * 64 - first - c;
+#pragma unroll
+              for (int j = 0; j < 2 * MT; ++j) {
+                if (8 * j > lim0) s[j >> 1][nt][(j & 1) * 2] = -INFINITY;
+                if (8 * j > lim1) s[j >> 1][nt][(j & 1) * 2 + 1] = -INFINITY;
+              }
+            }
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mx0 = fmax3(mx0, s[mt][nt][0], s[mt][nt][2]);
+              mx1 = fmax3(mx1, s[mt][nt][1], s[mt][nt][3]);
+            }
+#pragma unroll
+            for (int x = 4; x <= 16; x <<= 1) {
+              mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+              mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+            }
+            const float2 C = *reinterpret_cast<const float2*>(row_c + r);
+            const float n0 = fmaxf(m[nt].x, mx0 * C.x), n1 = fmaxf(m[nt].y, mx1 * C.y);
+            const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+            if (__any_sync(0xffffffffu, n0 != m[nt].x || n1 != m[nt].y)) {
+              const float2 al = make_float2(ex2_approx(m[nt].x - u0), ex2_approx(m[nt].y - u1));
+              m[nt] = make_float2(n0, n1);
+              l[nt] = __fmul2_rn(l[nt], al);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                  const float2 v = __fmul2_rn(make_float2(o[nt][i][k], o[nt][i][k + 1]), al);
+                  o[nt][i][k] = v.x;
+                  o[nt][i][k + 1] = v.y;
+                }
+            }
+            const float2 bias = make_float2(kPShift - u0, kPShift - u1);
+#pragma unroll
+            for (int j = 0; j < 2 * MT; ++j) {
+              float2 x = __ffma2_rn(make_float2(s[j >> 1][nt][(j & 1) * 2], s[j >> 1][nt][(j & 1) * 2 + 1]), C, bias);
+              x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+              l[nt] = __fadd2_rn(l[nt], x);
+              pb[j >> 1][nt][j & 1] = transpose8x8(pack_half2(x.x, x.y));
+            }
+          }
+          // ---- O^T += V^T P^T: MT steps of 16 tokens ----
+#pragma unroll
+          for (int kt = 0; kt < MT; ++kt) {
+            const int r0 = first / 2 + kt * 8 + t;                     // this thread's token pairs: r0, r0 + 4
+            const uint4 va = *reinterpret_cast<const uint4*>(sp + L::OFF_V + r0 * 128 + c * 16);
+            const uint4 vb = *reinterpret_cast<const uint4*>(sp + L::OFF_V + (r0 + 4) * 128 + c * 16);
+            uint32_t sca = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + r0 * 2);
+            uint32_t scb = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + (r0 + 4) * 2);
+            if (p * 64 + 64 > g.q.ctx) {                   // slots behind the context: weight 0, value 0
+              const int left = g.q.ctx - p * 64;           // valid slots of the page
+              if (2 * r0 >= left) sca = 0; else if (2 * r0 + 1 >= left) sca &= 0xFFu;
+              if (2 * r0 + 8 >= left) scb = 0; else if (2 * r0 + 9 >= left) scb &= 0xFFu;
+            }
+            const __half2 fa = e4m3x2_to_half2(sca), fb = e4m3x2_to_half2(scb);
+            const uint32_t* vaw = reinterpret_cast<const uint32_t*>(&va);
+            const uint32_t* vbw = reinterpret_cast<const uint32_t*>(&vb);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t ha[4], hb[4];
+              e2m1x8_to_half2(vaw[w], ha);
+              e2m1x8_to_half2(vbw[w], hb);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) { ha[k] = hmul2(ha[k], fa); hb[k] = hmul2(hb[k], fb); }
+              const uint32_t a0[4] = {ha[0], ha[1], hb[0], hb[1]}, a1[4] = {ha[2], ha[3], hb[2], hb[3]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16816(o[nt][2 * w], a0, pb[kt][nt][0], pb[kt][nt][1]);
+                mma16816(o[nt][2 * w + 1], a1, pb[kt][nt][0], pb[kt][nt][1]);
               }
             }
           }
         }
-        // ---- softmax: this thread's rows are 2 t, 2 t + 1 of each tile, its tokens c + 8 j ----
-        uint32_t pb[2][NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float x[2][4];                                 // [row][token c + 8 j]
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[0][j] = s[j >> 1][nt][(j & 1) * 2] * C[nt][0];
-            x[1][j] = s[j >> 1][nt][(j & 1) * 2 + 1] * C[nt][1];
-          }
-          if (base + 31 > lim_min) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (base + c + 8 * j > lim[nt][0]) x[0][j] = -INFINITY;
-              if (base + c + 8 * j > lim[nt][1]) x[1][j] = -INFINITY;
-            }
-          }
-          float alpha[2], bias[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float mx = fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m[nt][k], mx);
-            const float m_use = m_new == -INFINITY ? 0.f : m_new;
-            alpha[k] = ex2_approx(m[nt][k] - m_use);     // 0 before the first key
-            m[nt][k] = m_new;
-            bias[k] = kPShift - m_use;
-          }
-          if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-            l[nt][0] *= alpha[0];
-            l[nt][1] *= alpha[1];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              o[nt][i][0] *= alpha[0]; o[nt][i][1] *= alpha[1];
-              o[nt][i][2] *= alpha[0]; o[nt][i][3] *= alpha[1];
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float p0 = ex2_approx(x[0][j] + bias[0]), p1 = ex2_approx(x[1][j] + bias[1]);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            pb[j >> 1][nt][j & 1] = transpose8x8(pack_half2(p0, p1));
-          }
-        }
-        // ---- O^T += V^T P^T: two steps of 16 tokens ----
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const int r0 = half * 16 + kt * 8 + t;         // this thread's token pairs: r0, r0 + 4
-          const uint4 va = *reinterpret_cast<const uint4*>(sp + L::OFF_V + r0 * 128 + c * 16);
-          const uint4 vb = *reinterpret_cast<const uint4*>(sp + L::OFF_V + (r0 + 4) * 128 + c * 16);
-          uint32_t sca = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + r0 * 2);
-          uint32_t scb = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + (r0 + 4) * 2);
-          if (base + 32 > g.q.ctx) {                     // slots behind the context: weight 0, value 0
-            const int left = g.q.ctx - p * 64;           // valid slots of the page
-            if (2 * r0 >= left) sca = 0; else if (2 * r0 + 1 >= left) sca &= 0xFFu;
-            if (2 * r0 + 8 >= left) scb = 0; else if (2 * r0 + 9 >= left) scb &= 0xFFu;
-          }
-          const __half2 fa = e4m3x2_to_half2(sca), fb = e4m3x2_to_half2(scb);
-          const uint32_t* vaw = reinterpret_cast<const uint32_t*>(&va);
-          const uint32_t* vbw = reinterpret_cast<const uint32_t*>(&vb);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t ha[4], hb[4];
-            e2m1x8_to_half2(vaw[w], ha);
-            e2m1x8_to_half2(vbw[w], hb);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) { ha[k] = hmul2(ha[k], fa); hb[k] = hmul2(hb[k], fb); }
-            const uint32_t a0[4] = {ha[0], ha[1], hb[0], hb[1]}, a1[4] = {ha[2], ha[3], hb[2], hb[3]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma16816(o[nt][2 * w], a0, pb[kt][nt][0], pb[kt][nt][1]);
-              mma16816(o[nt][2 * w + 1], a1, pb[kt][nt][0], pb[kt][nt][1]);
-            }
-          }
-        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + st);
+      __syncwarp();                                      // the stage has been read
+      if (p + L::WARPS < g.p1) {
+        const bool good = load_page(st, next);
+        (st ? ok1 : ok0) = good;
+      } else {
+        owed = true;                                     // its O goes there first
+      }
+      st ^= 1;
     }
+    gi += g.p1 - g.p0;
 
-    // ---- the eight warps' results joined, eight rows at a time ----
+    // ---- the warps' results joined, eight rows at a time ----
     const bool whole = g.p0 == 0 && g.p1 == g.np;
-    float* mbuf = reinterpret_cast<float*>(sm + L::OFF_M);
+    float* mbuf = reinterpret_cast<float*>(ring + (st ^ 1) * L::STAGE);
+    int* at = reinterpret_cast<int*>(sm + L::OFF_AT);
+    if (lane == 0) at[warp] = owed ? static_cast<int>(reinterpret_cast<unsigned char*>(mbuf) - sm) : -1;
     float2* mlbuf = reinterpret_cast<float2*>(sm + L::OFF_ML);
     float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (g.p0 > 0 ? 0 : 1)) * kKv4PartFloats;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0) named_bar_sync(1, L::WARPS * 32);
+      if (nt > 0) __syncthreads();
+#pragma unroll
+      for (int x = 4; x <= 16; x <<= 1) {
+        l[nt].x += __shfl_xor_sync(0xffffffffu, l[nt].x, x);
+        l[nt].y += __shfl_xor_sync(0xffffffffu, l[nt].y, x);
+      }
+      if (c == 0) {
+        mlbuf[warp * 8 + 2 * t] = make_float2(m[nt].x, l[nt].x);
+        mlbuf[warp * 8 + 2 * t + 1] = make_float2(m[nt].y, l[nt].y);
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float ls = l[nt][k];
-        ls += __shfl_xor_sync(0xffffffffu, ls, 4);
-        ls += __shfl_xor_sync(0xffffffffu, ls, 8);
-        ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-        if (c == 0) mlbuf[warp * 8 + 2 * t + k] = make_float2(m[nt][k], ls);
-        float* dst = mbuf + (warp * 8 + 2 * t + k) * L::M_LD + c * 16;   // channels 16 c + 2 i, + 1
+        if (!owed) break;                                // no page of this pair: nothing to join
+        float* dst = mbuf + (2 * t + k) * L::M_LD + c * 16;   // channels 16 c + 2 i, + 1
 #pragma unroll
         for (int i = 0; i < 8; i += 2)
           *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[nt][i][k], o[nt][i][2 + k], o[nt][i + 1][k], o[nt][i + 1][2 + k]);
       }
-      named_bar_sync(1, L::WARPS * 32);
-      const int r = nt * 8 + warp;                       // a warp joins one row, a lane four channels
-      if (r < rows) {
+      __syncthreads();
+      for (int rr = warp; rr < 8; rr += L::WARPS) {       // a warp joins a row, a lane four channels
+        const int r = nt * 8 + rr;
+        if (r >= rows) break;
         float M = -INFINITY, ls = 0.f;
 #pragma unroll
-        for (int k = 0; k < L::WARPS; ++k) M = fmaxf(M, mlbuf[k * 8 + warp].x);
+        for (int k = 0; k < L::WARPS; ++k) M = fmaxf(M, mlbuf[k * 8 + rr].x);
         const float mu = M == -INFINITY ? 0.f : M;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < L::WARPS; ++k) {
-          const float2 ml = mlbuf[k * 8 + warp];
+          if (at[k] < 0) continue;
+          const float2 ml = mlbuf[k * 8 + rr];
           const float wgt = ex2_approx(ml.x - mu);
-          const float4 v = *reinterpret_cast<const float4*>(mbuf + (k * 8 + warp) * L::M_LD + lane * 4);
+          const float4 v = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(sm + at[k]) + rr * L::M_LD + lane * 4);
           ls += wgt * ml.y;
           acc.x += wgt * v.x; acc.y += wgt * v.y; acc.z += wgt * v.z; acc.w += wgt * v.w;
         }

@@ -868,7 +868,7 @@ Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
   s.nt = r <= 8 ? 1 : r <= 16 ? 2 : 4;
   s.rows_max = 8 * s.nt;
   const int64_t units = static_cast<int64_t>(p->num_seqs) * ((p->max_context + 63) / 64) * p->cache.kv_heads;
-  const int64_t ctas = static_cast<int64_t>(sm_count()) * (s.nt == 1 ? 2 : 1);
+  const int64_t ctas = sm_count();
   s.split_ctas = static_cast<int>(ctas < (units + 3) / 4 ? ctas : (units + 3) / 4);
   s.part_off = (4 * (static_cast<size_t>(p->num_seqs) + 1) + 15) / 16 * 16;
   s.bytes = s.part_off + static_cast<size_t>(s.split_ctas) * 2 * kKv4PartFloats * 4;

@@ -117,7 +117,7 @@ def timeout_site() -> dict | None:
     v = _lib.load().qk4v8_timeout_site()
     if v == 0:
         return None
-    return {"kernel": {1: "attn_fwd", 2: "decode", 3: "selftest"}.get(v >> 56, v >> 56),
+    return {"kernel": {1: "attn_fwd", 2: "decode", 3: "selftest", 4: "kv4_prompt"}.get(v >> 56, v >> 56),
             "role": {0: "producer", 1: "mma", 2: "softmax"}.get((v >> 48) & 0xFF, (v >> 48) & 0xFF),
             "barrier": (v >> 40) & 0xFF, "tile": (v >> 20) & 0xFFFFF, "block": v & 0xFFFFF}
 

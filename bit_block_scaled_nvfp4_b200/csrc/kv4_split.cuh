@@ -50,8 +50,10 @@ struct Kv4AttnArgs {
   float softmax_scale;
   void* out;
   float* lse;
-  int32_t* plan;             // workspace: [0] units a CTA, [1 + s] first unit of sequence s
-  float* part;               // workspace: partials, two a CTA
+  int64_t* plan;             // workspace: the split kernel's kv4_range plan
+  float* part;               // workspace: its partials, two a CTA
+  int64_t* prompt_plan;      // the same of the prompt kernel
+  float* prompt_part;
 };
 
 constexpr float kPShift = 6.f;
@@ -72,6 +74,67 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4AttnArgs& a, int s, bool flag
     q.n = 0;
   }
   return q;
+}
+
+// A CTA's part of a line of units that the sequences fill one after another: from unit `first` of
+// sequence s on, `left` units.
+struct Kv4Range {
+  int64_t sums[16];          // of the warps, while it is found
+  int64_t first;
+  int s, left;
+};
+// Cuts the line into equal parts of at least `least` units, one a CTA, and finds this CTA's. weight(i):
+// units of sequence i. plan[0] gets the units a CTA, plan[1 + i] the first unit of sequence i (for
+// the kernels that join partials). Two passes over the sequences: the total, then the place.
+template <int THREADS, typename W>
+__device__ __forceinline__ void kv4_range(W weight, int S, int least, int64_t* plan, Kv4Range* r) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int64_t w = 0, before = 0, total = 0, first = 0, per = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t run = 0;
+    if (pass == 1) {
+      per = (total + gridDim.x - 1) / gridDim.x;
+      if (per < least) per = least;
+      first = per * blockIdx.x;
+      if (first > total) first = total;
+      if (tid == 0) {
+        r->s = S;
+        r->first = 0;
+        r->left = static_cast<int>(per < total - first ? per : total - first);
+        if (blockIdx.x == 0) plan[0] = per;
+      }
+      __syncthreads();
+    }
+    for (int i0 = 0; i0 < S; i0 += THREADS) {
+      const int i = i0 + tid;
+      if (pass == 0 || S > THREADS) {                    // a single chunk is kept from pass 0
+        w = i < S ? weight(i) : 0;
+        int64_t x = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) r->sums[warp] = x;
+        __syncthreads();
+        before = x - w;
+        int64_t sum = 0;
+#pragma unroll
+        for (int k = 0; k < THREADS / 32; ++k) {
+          if (k < warp) before += r->sums[k];
+          sum += r->sums[k];
+        }
+        if (pass == 0) total += sum;
+        else { before += run; run += sum; }
+      }
+      if (pass == 1 && i < S) {
+        if (blockIdx.x == 0) plan[1 + i] = before;
+        if (w > 0 && first >= before && first < before + w) { r->s = i; r->first = first - before; }
+      }
+    }
+  }
+  __syncthreads();
 }
 
 // A position in the line of units (a unit: one page of one KV head of a sequence; sequence by
@@ -120,8 +183,8 @@ struct Kv4SplitLayout {
   static constexpr int OFF_Q = WARPS * NS * STAGE;
   static constexpr int OFF_ML = OFF_Q + ROWS * Q_LD;    // [warp][8 rows] (m, l)
   static constexpr int OFF_ROW = OFF_ML + WARPS * 8 * 8;        // [ROWS] C, then [ROWS] limit
-  static constexpr int OFF_MISC = OFF_ROW + ROWS * 8;   // [12] warp sums, [3] start of the range
-  static constexpr int OFF_AT = OFF_MISC + 64;          // [warp] where its O lies in the join
+  static constexpr int OFF_RANGE = OFF_ROW + ROWS * 8;
+  static constexpr int OFF_AT = OFF_RANGE + sizeof(Kv4Range);   // [warp] where its O lies in the join
   static constexpr int SMEM = OFF_AT + WARPS * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(8 * M_LD * 4 <= STAGE, "a stage holds a warp's O of eight rows");
@@ -182,65 +245,24 @@ kv4_split_kernel(Kv4AttnArgs a) {
   using L = Kv4SplitLayout<NT>;
   extern __shared__ __align__(128) unsigned char kv4_smem[];
   unsigned char* sm = kv4_smem;
-  int* misc = reinterpret_cast<int*>(sm + L::OFF_MISC);
+  Kv4Range* rng = reinterpret_cast<Kv4Range*>(sm + L::OFF_RANGE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.Hq / a.c.Hkv;
 
-  // ---- this CTA's range of units ----
-  auto weight = [&](int s) -> int {
-    if (s >= a.S) return 0;
-    const Kv4Seq q = kv4_seq(a, s, blockIdx.x == 0);
-    return (q.n > 0 && q.n * group <= a.rows_max) ? ((q.ctx + 63) >> 6) * a.c.Hkv : 0;
-  };
-  int w0 = 0, total = 0, excl = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    // pass 0: the total; pass 1 (the same sums again): the sequence that holds the first unit
-    int run = 0, first = 0;
-    if (pass == 1) {
-      const int per = max(4, (total + gridDim.x - 1) / static_cast<int>(gridDim.x));
-      first = min(static_cast<int64_t>(per) * blockIdx.x, static_cast<int64_t>(total));
-      if (tid == 0) {
-        misc[12] = a.S; misc[13] = 0; misc[14] = min(per, total - first);
-        if (blockIdx.x == 0) a.plan[0] = per;
-      }
-      __syncthreads();
-    }
-    for (int s0 = 0; s0 < a.S; s0 += L::THREADS) {
-      if (pass == 0 || a.S > L::THREADS) {               // one chunk: kept from pass 0
-        w0 = weight(s0 + tid);
-        int x = w0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) misc[warp] = x;
-        __syncthreads();
-        excl = x - w0;
-        int sum = 0;
-        for (int i = 0; i < L::WARPS; ++i) {
-          if (i < warp) excl += misc[i];
-          sum += misc[i];
-        }
-        if (pass == 0) total += sum;
-        else { excl += run; run += sum; }
-      }
-      if (pass == 1 && s0 + tid < a.S) {
-        if (blockIdx.x == 0) a.plan[1 + s0 + tid] = excl;
-        if (w0 > 0 && first >= excl && first < excl + w0) { misc[12] = s0 + tid; misc[13] = first - excl; }
-      }
-    }
-  }
-  __syncthreads();
+  kv4_range<L::THREADS>(
+      [&](int i) -> int64_t {
+        const Kv4Seq q = kv4_seq(a, i, blockIdx.x == 0);
+        return (q.n > 0 && q.n * group <= a.rows_max) ? static_cast<int64_t>((q.ctx + 63) >> 6) * a.c.Hkv : 0;
+      },
+      a.S, 4, a.plan, rng);
   Kv4Walk walk;                                         // the pair at hand
-  walk.s = misc[12];
-  walk.left = misc[14];
+  walk.s = rng->s;
+  walk.left = rng->left;
   walk.h = walk.p = 0;
   walk.find(a);
   if (walk.left > 0) {
-    walk.h = misc[13] / walk.np;
-    walk.p = misc[13] % walk.np;
+    walk.h = static_cast<int>(rng->first / walk.np);
+    walk.p = static_cast<int>(rng->first % walk.np);
   }
   Kv4Walk ahead = walk;                                 // the next page this warp loads
   ahead.advance(a, warp);
@@ -541,9 +563,9 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(Kv4AttnArgs a) {
   const int group = a.Hq / a.c.Hkv;
   const Kv4Seq q = kv4_seq(a, s, false);
   if (q.n <= 0 || q.n * group > a.rows_max || r >= q.n * group) return;
-  const int per = a.plan[0], np = (q.ctx + 63) >> 6;
-  const int first = a.plan[1 + s] + h * np;
-  const int c0 = first / per, c1 = (first + np - 1) / per;
+  const int np = (q.ctx + 63) >> 6;
+  const int64_t per = a.plan[0], first = a.plan[1 + s] + static_cast<int64_t>(h) * np;
+  const int c0 = static_cast<int>(first / per), c1 = static_cast<int>((first + np - 1) / per);
   if (c0 == c1) return;                                 // written by the split kernel
   const int tid = threadIdx.x;
   auto part = [&](int cta) {

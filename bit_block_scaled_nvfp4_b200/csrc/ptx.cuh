@@ -23,7 +23,7 @@ __device__ __forceinline__ void flag_error(unsigned int bits) { atomicOr(&g_stat
 // First wait that timed out since the last read: kernel id << 56 | role << 48 |
 // barrier id << 40 | (tile & 0xFFFFF) << 20 | (blockIdx.x & 0xFFFFF). Zero when none.
 __device__ unsigned long long g_timeout_site = 0;
-enum : uint32_t { kKernelFwd = 1, kKernelDecode = 2, kKernelSelfTest = 3 };
+enum : uint32_t { kKernelFwd = 1, kKernelDecode = 2, kKernelSelfTest = 3, kKernelKv4Prompt = 4 };
 enum : uint32_t { kRoleProducer = 0, kRoleMma = 1, kRoleSoftmax = 2 };
 __device__ __forceinline__ uint64_t wait_site(uint32_t kernel, uint32_t role, uint32_t bar_id,
                                               int tile) {
@@ -318,6 +318,14 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// The same with A in TMEM (row = lane, two 16-bit elements a column).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 // Arrive on an mbarrier when every tcgen05 operation issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {

@@ -15,6 +15,7 @@
 #include "append.cuh"
 #include "kv4.cuh"
 #include "kv4_split.cuh"
+#include "kv4_prompt.cuh"
 #include "pages.cuh"
 
 using namespace qk4v8;
@@ -854,24 +855,39 @@ extern "C" qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* p, cudaStream_t s
 // ------------------------------------------------------------------------------------------
 namespace {
 struct Kv4Schedule {
+  bool split, prompt;     // which kernels run
   int nt;                 // split kernel: tiles of eight rows
-  int rows_max;           // sequences with at most this many rows a KV head go to it
-  int split_ctas;
-  size_t part_off, bytes; // workspace: plan, then the partials
+  int rows_max;           // sequences with at most this many rows a KV head go to it, others to the prompt kernel
+  int split_ctas, prompt_ctas;
+  size_t part_off, prompt_plan_off, prompt_part_off, bytes;   // workspace: plan and partials of each
 };
-// nt 1, 2 or 4: rows a KV head reads at once. Where every sequence has at most 32 rows the split
-// kernel takes them all; otherwise it takes the sequences of one token.
+// Where every sequence has at most 32 rows a KV head (query tokens times heads a group) the split
+// kernel takes them all. Otherwise it takes the sequences of one token (of a whole tile of rows,
+// to be exact), and the prompt kernel the others; a lone sequence is then the prompt kernel's
+// whatever its length, which saves the split kernel's two launches.
 Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
   Kv4Schedule s;
   const int64_t group = p->q_heads / p->cache.kv_heads, rows = p->max_q * group;
-  const int64_t r = rows <= 32 ? rows : group;
+  s.prompt = rows > 32;
+  s.split = !s.prompt || p->num_seqs > 1;
+  const int64_t r = s.prompt ? group : rows;
   s.nt = r <= 8 ? 1 : r <= 16 ? 2 : 4;
-  s.rows_max = 8 * s.nt;
-  const int64_t units = static_cast<int64_t>(p->num_seqs) * ((p->max_context + 63) / 64) * p->cache.kv_heads;
-  const int64_t ctas = sm_count();
-  s.split_ctas = static_cast<int>(ctas < (units + 3) / 4 ? ctas : (units + 3) / 4);
-  s.part_off = (4 * (static_cast<size_t>(p->num_seqs) + 1) + 15) / 16 * 16;
-  s.bytes = s.part_off + static_cast<size_t>(s.split_ctas) * 2 * kKv4PartFloats * 4;
+  s.rows_max = s.split ? 8 * s.nt : 0;
+  const int64_t heads = static_cast<int64_t>(p->num_seqs) * p->cache.kv_heads, sms = sm_count();
+  auto ctas = [&](int64_t units, int64_t least) {
+    const int64_t n = (units + least - 1) / least;
+    return static_cast<int>(sms < n ? sms : n);
+  };
+  s.split_ctas = ctas(heads * ((p->max_context - 1) / 64 + 1), 4);
+  const int64_t tokens = 2 * (128 / group), items = (p->max_q - 1) / tokens + 1;
+  const int64_t tiles = (p->max_context - 1) / 128 + 1;
+  s.prompt_ctas = ctas(heads > sms || items > sms || tiles > sms ? sms * 2 : heads * items * tiles, 2);
+  const size_t plan = (8 * (static_cast<size_t>(p->num_seqs) + 1) + 15) / 16 * 16;
+  s.part_off = plan;
+  s.prompt_plan_off = s.split ? s.part_off + static_cast<size_t>(s.split_ctas) * 2 * kKv4PartFloats * 4 : 0;
+  s.prompt_part_off = s.prompt_plan_off + plan;
+  s.bytes = s.prompt ? s.prompt_part_off + static_cast<size_t>(s.prompt_ctas) * 2 * kPromptPartFloats * 4
+                     : s.prompt_plan_off;
   return s;
 }
 
@@ -904,15 +920,36 @@ qk4v8_status launch_kv4_split(const Kv4AttnArgs& a, int ctas, cudaStream_t strea
 }
 
 template <typename T>
+qk4v8_status launch_kv4_prompt(const Kv4AttnArgs& a, int ctas, cudaStream_t stream) {
+  using L = PromptLayout;
+  // as for the other prefill kernels: the launch's register count has to be the one that the
+  // setmaxnreg split is computed from
+  static PerDeviceOnce opt_in;
+  if (!opt_in.run(current_device(), [] {
+        cudaFuncAttributes fa;
+        return set_smem(kv4_prompt_kernel<T>, L::SMEM_ALLOC) &&
+               cudaFuncGetAttributes(&fa, kv4_prompt_kernel<T>) == cudaSuccess && fa.numRegs == L::REGS_LAUNCH;
+      }))
+    return QK4V8_ERR_CUDA;
+  kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_ALLOC, stream>>>(a);
+  if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
+  if (ctas > 1) kv4_prompt_merge_kernel<T><<<dim3(ctas - 1, 8), 256, 0, stream>>>(a);
+  return launch_status();
+}
+
+template <typename T>
 qk4v8_status launch_kv4_attn(const qk4v8_kv4_attn_params* p, const Kv4Schedule& sc, const Kv4AttnArgs& a,
                              cudaStream_t stream) {
-  const qk4v8_status st = sc.nt == 1   ? launch_kv4_split<1, T>(a, sc.split_ctas, stream)
-                          : sc.nt == 2 ? launch_kv4_split<2, T>(a, sc.split_ctas, stream)
-                                       : launch_kv4_split<4, T>(a, sc.split_ctas, stream);
-  if (st != QK4V8_OK) return st;
-  const dim3 grid(static_cast<unsigned>(p->num_seqs * p->cache.kv_heads), static_cast<unsigned>(sc.rows_max));
-  kv4_merge_kernel<T><<<grid, 128, 0, stream>>>(a);
-  return launch_status();
+  if (sc.split) {
+    const qk4v8_status st = sc.nt == 1   ? launch_kv4_split<1, T>(a, sc.split_ctas, stream)
+                            : sc.nt == 2 ? launch_kv4_split<2, T>(a, sc.split_ctas, stream)
+                                         : launch_kv4_split<4, T>(a, sc.split_ctas, stream);
+    if (st != QK4V8_OK) return st;
+    const dim3 grid(static_cast<unsigned>(p->num_seqs * p->cache.kv_heads), static_cast<unsigned>(sc.rows_max));
+    kv4_merge_kernel<T><<<grid, 128, 0, stream>>>(a);
+    if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
+  }
+  return sc.prompt ? launch_kv4_prompt<T>(a, sc.prompt_ctas, stream) : QK4V8_OK;
 }
 }  // namespace
 
@@ -925,7 +962,6 @@ extern "C" qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* p, void* wor
   if (const qk4v8_status st = check_kv4_attn(p); st != QK4V8_OK) return st;
   if (p->total_q == 0) return QK4V8_OK;
   const Kv4Schedule sc = kv4_schedule(p);
-  if (static_cast<int64_t>(p->max_q) * (p->q_heads / p->cache.kv_heads) > 32) return QK4V8_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < sc.bytes) return QK4V8_ERR_INVALID_ARG;
   Kv4AttnArgs a;
   a.c = kv4_cache(p->cache);
@@ -933,8 +969,11 @@ extern "C" qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* p, void* wor
   a.total_q = p->total_q; a.S = p->num_seqs; a.max_pages = p->max_pages; a.Hq = p->q_heads; a.max_q = p->max_q;
   a.max_context = p->max_context; a.rows_max = sc.rows_max; a.softmax_scale = p->softmax_scale;
   a.out = p->out; a.lse = p->lse;
-  a.plan = static_cast<int32_t*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + sc.part_off);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.plan = reinterpret_cast<int64_t*>(ws);
+  a.part = reinterpret_cast<float*>(ws + sc.part_off);
+  a.prompt_plan = reinterpret_cast<int64_t*>(ws + sc.prompt_plan_off);
+  a.prompt_part = reinterpret_cast<float*>(ws + sc.prompt_part_off);
   return p->dtype == QK4V8_BF16 ? launch_kv4_attn<__nv_bfloat16>(p, sc, a, stream)
                                 : launch_kv4_attn<__half>(p, sc, a, stream);
 }

@@ -64,7 +64,7 @@ qk4v8_status qk4v8_check_status(cudaStream_t stream);
 
 /*
  * Where the first device wait that timed out since the last call sat, then cleared (0 when
- * none): kernel << 56 (1 prefill, 2 decode) | role << 48 (0 producer warp, 1 MMA issuer,
+ * none): kernel << 56 (1 prefill, 2 decode, 4 prompts over the 4-bit cache) | role << 48 (0 producer warp, 1 MMA issuer,
  * 2 softmax warps) | barrier index << 40 | (key tile & 0xFFFFF) << 20 | (block & 0xFFFFF).
  * Synchronous; call it after qk4v8_check_status() reported QK4V8_ERR_TIMEOUT.
  */

@@ -128,3 +128,28 @@ def test_more_sequences_than_a_block_counts_at_once():
     c = Case([0 if i % 7 == 3 else 1 for i in range(700)], past, 2, 1, torch.bfloat16)
     out, lse = c.run(max_q=1)
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hq,hkv,new,past", [
+    (1, 1, [200], [0]), (4, 1, [128], [0]), (2, 2, [129, 33], [0, 0]), (8, 2, [300], [1000]),
+    (6, 2, [130, 77, 1], [5, 700, 64]), (7, 1, [90, 0, 40], [63, 9, 1]), (16, 1, [70, 5], [129, 2]),
+    (5, 1, [257, 51, 52], [0, 31, 128]), (26, 2, [41, 200], [333, 0])])
+def test_prompts_and_chunks(dtype, hq, hkv, new, past):
+    c = Case(new, past, hq, hkv, dtype, seed=len(new) + hq)
+    c.check(*c.run())
+
+
+def test_a_long_prompt():
+    c = Case([3000], [0], 8, 2, torch.bfloat16)
+    c.check(*c.run())
+
+
+def test_a_chunk_far_into_a_long_context():
+    c = Case([100], [20000], 8, 2, torch.float16)
+    c.check(*c.run())
+
+
+def test_steps_and_chunks_together():
+    c = Case([1, 150, 1, 0, 1, 2, 90, 1], [700, 100, 64, 5, 2000, 0, 0, 127], 16, 4, torch.bfloat16)
+    c.check(*c.run())

@@ -1,8 +1,8 @@
 // Attention of many query rows per KV head over the 4-bit cache: prompts and chunks of prompts.
 //
-// Mathematics as in kv4_split.cuh (Q to fp16 by a power of two per row, K and V decoded exactly to
-// fp16, FP32 scores, online softmax, P = fp16(2^(s - m + 6)), FP32 O and l) on the fp16 tensor
-// cores of tcgen05. The running maximum that P and O refer to follows the true one only when it
+// Mathematics as in kv4_split.cuh (exact products of Q with K, FP32 scores, online softmax,
+// P = fp16(2^(s - m + 6)), FP32 O and l) on the 16-bit tensor cores of tcgen05. Q is taken as it is and K
+// decoded into Q's type, fp16 or bf16, exactly either way; V is decoded to fp16. The running maximum that P and O refer to follows the true one only when it
 // has risen by more than 2^8 (so P stays below 2^14): O in tensor memory is rarely rescaled.
 //
 // A work item is a KV head of a sequence and up to 256 query rows of it, rows being (token, head of
@@ -24,23 +24,6 @@
 
 namespace qk4v8 {
 
-struct PromptLayout {
-  static constexpr int OFF_Q = 0;                        // [unit] 2 x 16 KB (64 channels each)
-  static constexpr int OFF_K = 65536;                    // [stage] 2 x 16 KB (64 channels each)
-  static constexpr int OFF_V = OFF_K + 65536;            // [stage] 2 x 16 KB (64 tokens each)
-  static constexpr int OFF_ROW = OFF_V + 65536;          // [256] C, then [256] last key seen
-  static constexpr int OFF_FLAG = OFF_ROW + 2048;        // [8] pages missing, by tile
-  static constexpr int OFF_RANGE = OFF_FLAG + 32;
-  static constexpr int OFF_BAR = OFF_RANGE + (sizeof(Kv4Range) + 7) / 8 * 8;
-  static constexpr int N_BARS = 18;
-  static constexpr int SMEM_BYTES = OFF_BAR + N_BARS * 8 + 16;
-  static constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
-  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
-  static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1
-  static constexpr int THREADS = 512;
-  static constexpr int REGS_LAUNCH = 128, REGS_ISSUE = 56, REGS_DECODE = 104, REGS_SOFTMAX = 176;
-  static_assert(REGS_ISSUE + REGS_DECODE + 2 * REGS_SOFTMAX <= 4 * REGS_LAUNCH, "register split");
-};
 constexpr float kRiseLimit = 8.f;                        // log2 of how far the maximum may rise unfollowed
 constexpr int kPromptPartFloats = 256 * (kKv4D + 2);     // a partial: O, then m, then l of 256 rows
 
@@ -74,9 +57,33 @@ struct PromptSeq {
   }
 };
 
+// A CTA's part of an item, as the scheduling warp hands it to the others.
 struct PromptSeg {
-  PromptSeq sq;
-  int s, h, i, j0, j1, nt;                               // item i, key tiles [j0, j1) of nt
+  int s, h, q0, n, ctx;                                  // sequence, KV head; its first row, tokens, context
+  int tok;                                               // the item's first token
+  int j0, len;                                           // its key tiles j0 .. j0 + len - 1
+  int mine0, mine1;                                      // how many of them unit 0 and 1 see
+  int whole, first;                                      // the whole item; it begins here
+};                                                       // (s = -1: no more)
+struct PromptLayout {
+  static constexpr int OFF_Q = 0;                        // [unit] 2 x 16 KB (64 channels each)
+  static constexpr int OFF_K = 65536;                    // [stage] 2 x 16 KB (64 channels each)
+  static constexpr int OFF_V = OFF_K + 65536;            // [stage] 2 x 16 KB (64 tokens each)
+  static constexpr int OFF_MAP = OFF_V + 65536;          // [128] a row's token and head within the unit
+  static constexpr int OFF_FLAG = OFF_MAP + 256;        // [8] pages missing, by tile
+  static constexpr int OFF_RANGE = OFF_FLAG + 32;
+  static constexpr int OFF_BAR = OFF_RANGE + (sizeof(Kv4Range) + 7) / 8 * 8;
+  static constexpr int NSEG = 4;                         // segments handed out ahead
+  static constexpr int N_BARS = 17 + 2 * NSEG;
+  static constexpr int OFF_SEG = (OFF_BAR + N_BARS * 8 + 16 + 15) / 16 * 16;
+  static constexpr int SMEM_BYTES = OFF_SEG + NSEG * 64;
+  static_assert(sizeof(PromptSeg) <= 64, "a segment's slot");
+  static constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
+  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
+  static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1
+  static constexpr int THREADS = 512;
+  static constexpr int REGS_LAUNCH = 128, REGS_ISSUE = 80, REGS_DECODE = 80, REGS_SOFTMAX = 176;
+  static_assert(REGS_ISSUE + REGS_DECODE + 2 * REGS_SOFTMAX <= 4 * REGS_LAUNCH, "register split");
 };
 struct PromptWalk {
   PromptSeq sq;
@@ -109,10 +116,17 @@ struct PromptWalk {
   }
   __device__ __forceinline__ bool next(const Kv4AttnArgs& a, PromptSeg& g) {
     if (left <= 0) return false;
-    g.sq = sq; g.s = s; g.h = h; g.i = i; g.j0 = j;
-    g.nt = sq.tiles(i);
-    g.j1 = min(g.nt, j + left);
-    left -= g.j1 - j;
+    const int nt = sq.tiles(i), j1 = min(nt, j + left), TU = sq.T2 / 2;
+    g.s = s; g.h = h; g.q0 = sq.q.q0; g.n = sq.q.n; g.ctx = sq.q.ctx;
+    g.tok = i * sq.T2;
+    g.j0 = j; g.len = j1 - j;
+    const int nt0 = sq.tiles_to(min(sq.q.n, g.tok + TU));
+    const int nt1 = g.tok + TU < sq.q.n ? nt : 0;
+    g.mine0 = max(0, min(j1, nt0) - j);
+    g.mine1 = max(0, min(j1, nt1) - j);
+    g.whole = j == 0 && j1 == nt;
+    g.first = j == 0;
+    left -= j1 - j;
     j = 0;
     if (left > 0 && ++i == sq.items()) {
       i = 0;
@@ -125,12 +139,30 @@ struct PromptWalk {
     return true;
   }
 };
-// Key tiles that unit u of a segment's item sees (0: the unit has no tokens).
-__device__ __forceinline__ int unit_tiles(const PromptSeg& g, int u) {
-  const int t0 = g.i * g.sq.T2 + u * (g.sq.T2 / 2);
-  return t0 >= g.sq.q.n ? 0 : g.sq.tiles_to(min(g.sq.q.n, t0 + g.sq.T2 / 2));
-}
 
+// A block's scale times pairs of E2M1 values (as half2) in Q's type, exactly: in bf16 as
+// (value 2^-112) (scale 2^112), both and the product normal.
+template <typename T> struct KScale;
+template <> struct KScale<__half> {
+  __half2 f;
+  __device__ __forceinline__ explicit KScale(float s) : f(__float2half2_rn(s)) {}
+  __device__ __forceinline__ uint32_t times(uint32_t h) const { return hmul2(h, f); }
+};
+template <> struct KScale<__nv_bfloat16> {
+  __nv_bfloat162 f;
+  __device__ __forceinline__ explicit KScale(float s) : f(__float2bfloat162_rn(s * 0x1p112f)) {}
+  __device__ __forceinline__ uint32_t times(uint32_t h) const {
+    // the exponent field kept, fp16's bias of 15 read as bf16's of 127
+    const uint32_t b = ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
+// 16-byte asynchronous copy, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
+               : "memory");
+}
 template <typename T>
 __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   using L = PromptLayout;
@@ -147,18 +179,19 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   uint64_t* p_full = bars + 12;                          // [unit] P written, S read, O ready to add to
   uint64_t* o_full = bars + 14;                          // [unit] the segment's last PV is done
   uint64_t* mma_final = bars + 16;
-  uint64_t* rows_free = bars + 17;                       // both units have read the segment's row constants
+  uint64_t* seg_full = bars + 17;                        // [NSEG]
+  uint64_t* seg_empty = seg_full + L::NSEG;              // [NSEG]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Kv4Range* rng = reinterpret_cast<Kv4Range*>(sm + L::OFF_RANGE);
   volatile int* missing = reinterpret_cast<volatile int*>(sm + L::OFF_FLAG);
-  float* row_c = reinterpret_cast<float*>(sm + L::OFF_ROW);
-  int* row_lim = reinterpret_cast<int*>(sm + L::OFF_ROW) + 256;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.Hq / a.c.Hkv;
 
+  uchar2* row_map = reinterpret_cast<uchar2*>(sm + L::OFF_MAP);
+  if (threadIdx.x < 128) row_map[threadIdx.x] = make_uchar2(threadIdx.x / group, threadIdx.x % group);
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 3);
+    mbar_init(q_full, 2);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);
@@ -170,7 +203,10 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       mbar_init(o_full + i, 1);
     }
     mbar_init(mma_final, 1);
-    mbar_init(rows_free, 8);
+    for (int i = 0; i < L::NSEG; ++i) {
+      mbar_init(seg_full + i, 1);
+      mbar_init(seg_empty + i, 1 + 2 + 4 + 8);           // products, Q, decoding, softmax
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -189,9 +225,10 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       a.S, 2, a.prompt_plan, rng);
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  PromptWalk walk;
-  walk.start(a, rng);
-  PromptSeg g;
+  auto seg_at = [&](int seg) -> const PromptSeg& {
+    return *reinterpret_cast<const PromptSeg*>(sm + L::OFF_SEG + (seg % L::NSEG) * 64);
+  };
+  const int TU = 128 / group;                            // tokens of a unit
   const uint32_t role = warp == 0 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
   auto site = [&](uint64_t* bar, int tile) {
     return wait_site(kKernelKv4Prompt, role, static_cast<uint32_t>(bar - bars), tile);
@@ -208,52 +245,61 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         auto wait1 = [&](uint64_t* bar, uint32_t parity, int tile) -> bool {
           return bounded_wait(bar, parity, abort_flag, site(bar, tile));
         };
-        constexpr uint32_t idesc = idesc_f16(128, 128);
-        const uint32_t sQ = smem_u32(sm + L::OFF_Q), sK = smem_u32(sm + L::OFF_K), sV = smem_u32(sm + L::OFF_V);
+        constexpr uint32_t idesc_qk = idesc_f16(128, 128, std::is_same<T, __nv_bfloat16>::value);
+        constexpr uint32_t idesc_pv = idesc_f16(128, 128);
+        // descriptors of the first blocks; an offset of n bytes adds n / 16
+        const uint64_t dQ = make_sdesc(smem_u32(sm + L::OFF_Q), 16, 1024, kSw128);
+        const uint64_t dK = make_sdesc(smem_u32(sm + L::OFF_K), 16, 1024, kSw128);
+        const uint64_t dV = make_sdesc(smem_u32(sm + L::OFF_V), 16, 1024, kSw128);
         auto qk = [&](int u, int tile) {                 // S_u = Q_u K^T
+          const uint64_t q = dQ + u * 2048, k = dK + (tile & 1) * 2048;
+          const uint32_t tS = tbase + L::T_S + u * 128;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_f16(tbase + L::T_S + u * 128, make_sdesc(sQ + u * 32768 + off, 16, 1024, kSw128),
-                    make_sdesc(sK + (tile & 1) * 32768 + off, 16, 1024, kSw128), idesc, kk > 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
           mma_commit(s_full + u);
         };
         auto pv = [&](int u, int tile, bool first) {     // O_u += P_u V
+          const uint64_t v = dV + (tile & 1) * 2048;
+          const uint32_t tS = tbase + L::T_S + u * 128, tO = tbase + L::T_O + u * 128;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            mma_f16_ta(tbase + L::T_O + u * 128, tbase + L::T_S + u * 128 + kk * 8,
-                       make_sdesc(sV + (tile & 1) * 32768 + off, 16, 1024, kSw128), idesc, (first && kk == 0) ? 0u : 1u);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ta(tO, tS + kk * 8, v + (kk >> 2) * 1024 + (kk & 3) * 2, idesc_pv, (first && kk == 0) ? 0u : 1u);
         };
-        int tile = 0, n[2] = {0, 0};                     // tiles so far; of each unit
+        int tile = 0;
+        uint32_t odd = 0;                                // bit u: unit u's tiles so far, odd or even
         bool ok = true;
-        for (int seg = 0; ok && walk.next(a, g); ++seg) {
-          const int len = g.j1 - g.j0;
-          int mine[2];                                   // the segment's tiles of each unit
-          for (int u = 0; u < 2; ++u) mine[u] = max(0, min(g.j1, unit_tiles(g, u)) - g.j0);
+        for (int seg = 0;; ++seg) {
+          ok = wait1(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, tile);
+          if (!ok) break;
+          const int len = seg_at(seg).len, mine0 = seg_at(seg).mine0, mine1 = seg_at(seg).mine1;
+          const bool end = seg_at(seg).s < 0;
+          mbar_arrive(seg_empty + seg % L::NSEG);
+          if (end) break;
           ok = wait1(q_full, seg & 1, tile) && wait1(k_full + (tile & 1), (tile >> 1) & 1, tile);
           if (!ok) break;
           tc_fence_after();
+#pragma unroll 1
           for (int u = 0; u < 2; ++u)
-            if (mine[u] > 0) qk(u, tile);
+            if ((u ? mine1 : mine0) > 0) qk(u, tile);
           mma_commit(k_empty + (tile & 1));
           if (len == 1) mma_commit(q_empty);
           for (int t = 0; t < len && ok; ++t, ++tile) {
             bool v_in = false, k_in = false;
-            for (int u = 0; u < 2 && ok; ++u) {
-              if (t < mine[u]) {
-                ok = wait1(p_full + u, n[u] & 1, tile) &&
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+              const int mine = u ? mine1 : mine0;
+              if (t < mine) {
+                ok = wait1(p_full + u, (odd >> u) & 1, tile) &&
                      (v_in || wait1(v_full + (tile & 1), (tile >> 1) & 1, tile));
                 if (!ok) break;
                 v_in = true;
                 tc_fence_after();
                 pv(u, tile, t == 0);
-                ++n[u];
-                if (t + 1 == mine[u]) mma_commit(o_full + u);
+                odd ^= 1u << u;
+                if (t + 1 == mine) mma_commit(o_full + u);
               }
-              if (t + 1 < mine[u]) {
+              if (t + 1 < mine) {
                 ok = k_in || wait1(k_full + ((tile + 1) & 1), ((tile + 1) >> 1) & 1, tile);
                 if (!ok) break;
                 k_in = true;
@@ -266,69 +312,57 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
             if (t + 2 == len) mma_commit(q_empty);
             mma_commit(v_empty + (tile & 1));
           }
+          if (!ok) break;
         }
         mma_commit(mma_final);
         mbar_wait(mma_final, 0);
       }
       __syncwarp();
+    } else if (warp == 3) {
+      // ============================ segments (one thread) ============================
+      if (lane == 0) {
+        PromptWalk walk;
+        walk.start(a, rng);
+        bool more = true;
+        for (int seg = 0; more; ++seg) {
+          if (seg >= L::NSEG && !bounded_wait(seg_empty + seg % L::NSEG, (seg / L::NSEG - 1) & 1, abort_flag,
+                                              site(seg_empty + seg % L::NSEG, seg)))
+            break;
+          PromptSeg g;
+          more = walk.next(a, g);
+          if (!more) g.s = -1;
+          *reinterpret_cast<PromptSeg*>(sm + L::OFF_SEG + (seg % L::NSEG) * 64) = g;
+          mbar_arrive(seg_full + seg % L::NSEG);
+        }
+      }
+      __syncwarp();
     } else {
       // ================================ Q ================================
-      // Half a warp a row, 16 bytes a thread, eight rows in flight. The eights of channels are
-      // stored in K's order (see the decoding).
+      // Copied as it is, half a warp a row, 16 bytes a thread; rows without a token are zero. The
+      // eights of channels are stored in K's order (see the decoding).
       const int hw = lane >> 4, ch = lane & 15;
       const int pos = ((ch & 8) << 11) | (((ch & 7) ^ ((ch & 8) >> 2)) << 4);
-      bool ok = true;
-      for (int seg = 0; ok && walk.next(a, g); ++seg) {
-        const int TU = g.sq.T2 / 2;
-        bool waited = false;
-        for (int r0 = (warp - 1) * 16; r0 < 256 && ok; r0 += 48) {
-          uint4 u[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 2 * k + hw, ru = r & 127;
-            const int tok = g.i * g.sq.T2 + (r >> 7) * TU + ru / group;
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (ru < TU * group && tok < g.sq.q.n)
-              u[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (g.sq.q.q0 + tok) * a.q_stride +
-                                                          (g.h * group + ru % group) * kKv4D + ch * 8));
-          }
-          if (!waited) {
-            // the last segment's products have read Q, its softmax the constants
-            if (seg > 0 && !(waitw(q_empty, (seg - 1) & 1, seg) && waitw(rows_free, (seg - 1) & 1, seg))) {
-              ok = false;
-              break;
-            }
-            waited = true;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 2 * k + hw, ru = r & 127;
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(&u[k]);
-            float m = 0.f;
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = to_float2<T>(w[e]);
-              m = fmax3(m, fabsf(f.x), fabsf(f.y));
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float2 fac = kv4_row_factor<T>(m);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = to_float2<T>(w[e]);
-              h[e] = pack_half2(f.x * fac.x, f.y * fac.x);
-            }
-            *reinterpret_cast<uint4*>(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4))) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-            if (ch == 0) {
-              const int tok = g.i * g.sq.T2 + (r >> 7) * TU + ru / group;
-              row_c[r] = fac.y * (*a.c.k_ts * a.softmax_scale * kLog2e);
-              row_lim[r] = g.sq.q.ctx - g.sq.q.n + tok;
-            }
-          }
+      for (int seg = 0;; ++seg) {
+        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, seg)) break;
+        const PromptSeg& g = seg_at(seg);
+        if (g.s < 0) break;
+        const int left = g.n - g.tok;                    // tokens from the item's first on
+        const T* q = static_cast<const T*>(a.q) + (g.q0 + g.tok) * a.q_stride + g.h * group * kKv4D + ch * 8;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
+        // the last segment's products have read Q
+        if (seg > 0 && !waitw(q_empty, (seg - 1) & 1, seg)) break;
+#pragma unroll 4
+        for (int r = (warp - 1) * 2 + hw; r < 256; r += 4) {
+          const int ru = r & 127;
+          const uchar2 at = row_map[ru];
+          const int tok = (r >> 7) * TU + at.x;
+          const bool real = ru < TU * group && tok < left;
+          cp_async16_or_zero(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4)),
+                             real ? q + tok * a.q_stride + at.y * kKv4D : q, real);
         }
-        if (!ok) break;
+        cp_async_commit();
+        cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
@@ -347,20 +381,32 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     const int vp = tid >> 6, vt = tid & 7, vb = (tid >> 3) & 7;
     bool ok = true;
     int tile = 0;
-    // prefetched: page ids of the next tile, its K and (after K) its V
+    // prefetched: the next tile's page ids, its K and (after K) its V
     uint4 kc[4], vc[4];
     uint32_t ks[4];
     uint2 vs;
-    PromptSeg gn;
-    int jn = 0;
-    bool more = walk.next(a, gn);
-    if (more) jn = gn.j0;
-    int id0 = -1, id1 = -1, h = 0, ctx = 0, j = 0;       // the tile at hand
-    auto pages = [&](const PromptSeg& sg, int jj, int& p0, int& p1) {
-      const int np = (sg.sq.q.ctx + 63) >> 6;
-      const int32_t* row = a.table + static_cast<int64_t>(sg.s) * a.max_pages;
-      p0 = row[2 * jj];
-      p1 = 2 * jj + 1 < np ? row[2 * jj + 1] : -2;       // -2: behind the context, not missing
+    int v_left;                                          // this thread's V slots that lie in the context
+    // the tile at hand, and the next one's segment and place
+    int id0 = -1, id1 = -1, h = 0, ctx = 0, j = 0;
+    int seg = -1, jn = 0, j_end = 0;
+    // steps to the next tile: its page ids; false when there is none
+    auto next_tile = [&](int& p0, int& p1) -> bool {
+      if (++jn >= j_end) {
+        if (seg >= 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
+        }
+        ++seg;
+        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, tile) || seg_at(seg).s < 0) return false;
+        jn = seg_at(seg).j0;
+        j_end = jn + seg_at(seg).len;
+      }
+      // the second page may lie behind the context: the first again then, with no slot that counts
+      const int32_t* row = a.table + static_cast<int64_t>(seg_at(seg).s) * a.max_pages;
+      const int np = (seg_at(seg).ctx + 63) >> 6;
+      p0 = __ldg(row + 2 * jn);
+      p1 = __ldg(row + min(2 * jn + 1, np - 1));
+      return true;
     };
     auto valid = [&](int id) { return id >= 0 && id < a.c.num_pages; };
     auto load_k = [&]() {
@@ -388,34 +434,22 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           vc[i] = __ldg(reinterpret_cast<const uint4*>(a.c.v_pages + (head * 32 + vt * 4 + i) * 128 + vb * 16));
         vs = __ldg(reinterpret_cast<const uint2*>(a.c.v_scales + (head * 8 + vb) * 64 + vt * 8));
       }
-      // slots behind the context: value 0 (their weight is 0, but 0 x NaN is not)
-      const int left = ctx - (j * 128 + vp * 64 + vt * 8);
-      if (left < 8) {
-        const uint64_t keep = left <= 0 ? 0 : (1ull << (8 * left)) - 1;
-        vs.x &= static_cast<uint32_t>(keep);
-        vs.y &= static_cast<uint32_t>(keep >> 32);
-      }
+      v_left = ctx - (j * 128 + vp * 64 + vt * 8);
     };
     int n0 = -1, n1 = -1;                                // page ids of the tile after
+    bool more = next_tile(id0, id1);
     if (more) {
-      pages(gn, jn, id0, id1);
-      h = gn.h; ctx = gn.sq.q.ctx; j = jn;
+      h = seg_at(seg).h; ctx = seg_at(seg).ctx; j = jn;
       load_k();
     }
     while (more && ok) {
       const int stg = tile & 1;
-      // the tile after this one
-      bool after = true;
-      if (++jn >= gn.j1) {
-        after = walk.next(a, gn);
-        jn = after ? gn.j0 : 0;
-      }
-      if (after) pages(gn, jn, n0, n1);
+      const bool after = next_tile(n0, n1);
       // ---- K ----
       if (tile >= 2 && !waitw(k_empty + stg, ((tile >> 1) - 1) & 1, tile)) { ok = false; break; }
       load_v();
       if (tid == 0) {
-        const int gone = (valid(id0) ? 0 : 1) | (valid(id1) || id1 == -2 ? 0 : 2);
+        const int gone = (valid(id0) ? 0 : 1) | (valid(id1) ? 0 : 2);
         missing[tile & 7] = gone;
         if (gone) flag_error(kStatusBounds);
       }
@@ -423,7 +457,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       for (int i = 0; i < 4; ++i) {
         const int r = i * 32 + kr;
         const __half2 sc = e4m3x2_to_half2(ks[i]);
-        const __half2 f0 = __low2half2(sc), f1 = __high2half2(sc);
+        const KScale<T> f0(__low2float(sc)), f1(__high2float(sc));
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&kc[i]);
         unsigned char* row = sm + L::OFF_K + stg * 32768 + (kq >> 1) * 16384 + r * 128;
 #pragma unroll
@@ -431,7 +465,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           uint32_t d[4];
           e2m1x8_to_half2(w[e], d);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) d[x] = hmul2(d[x], e < 2 ? f0 : f1);
+          for (int x = 0; x < 4; ++x) d[x] = e < 2 ? f0.times(d[x]) : f1.times(d[x]);
           const int chunk = ((kq & 1) * 4 + (e ^ (kq & 2))) ^ (r & 7);
           *reinterpret_cast<uint4*>(row + chunk * 16) = make_uint4(d[0], d[1], d[2], d[3]);
         }
@@ -442,11 +476,16 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       // ---- V, with the next tile's K on its way ----
       id0 = n0; id1 = n1;
       if (after) {
-        h = gn.h; ctx = gn.sq.q.ctx; j = jn;
+        h = seg_at(seg).h; ctx = seg_at(seg).ctx; j = jn;
         load_k();
       }
       if (tile >= 2 && !waitw(v_empty + stg, ((tile >> 1) - 1) & 1, tile)) { ok = false; break; }
       {
+        if (v_left < 8) {                                // slots behind it: value 0 (weight 0 x NaN is not 0)
+          const uint64_t keep = v_left <= 0 ? 0 : (1ull << (8 * v_left)) - 1;
+          vs.x &= static_cast<uint32_t>(keep);
+          vs.y &= static_cast<uint32_t>(keep >> 32);
+        }
         const __half2 f[4] = {e4m3x2_to_half2(vs.x & 0xFFFFu), e4m3x2_to_half2(vs.x >> 16),
                               e4m3x2_to_half2(vs.y & 0xFFFFu), e4m3x2_to_half2(vs.y >> 16)};
         unsigned char* base = sm + L::OFF_V + stg * 32768 + vp * 16384 + vb * 16 * 128;
@@ -478,18 +517,17 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     const int wq = warp & 3, unit = (warp - 8) >> 2, row = wq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tbase + L::T_S + unit * 128 + lane_addr, tO = tbase + L::T_O + unit * 128 + lane_addr;
+    const float C = *a.c.k_ts * a.softmax_scale * kLog2e;
     bool ok = true;
     int tile = 0, n = 0, n_o = 0;                        // tiles; of this unit; segments with any
-    for (int seg = 0; ok && walk.next(a, g); ++seg) {
-      const int len = g.j1 - g.j0, nt_u = unit_tiles(g, unit);
-      const int mine = max(0, min(g.j1, nt_u) - g.j0);
-      if (!waitw(q_full, seg & 1, tile)) { ok = false; break; }
-      const float C = row_c[unit * 128 + row];
-      const int lim = row_lim[unit * 128 + row];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(rows_free);
-      const int t0 = g.i * g.sq.T2 + unit * (g.sq.T2 / 2);
-      const int lim_min = g.sq.q.ctx - g.sq.q.n + t0;     // keys every row of the unit sees
+    for (int seg = 0;; ++seg) {
+      if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, tile)) break;
+      const PromptSeg& g = seg_at(seg);
+      if (g.s < 0) break;
+      const int mine = unit == 0 ? g.mine0 : g.mine1;
+      const int t0 = g.tok + unit * TU;
+      const int lim = g.ctx - g.n + t0 + row_map[row].x - g.j0 * 128;   // the last key seen, from the segment's first
+      const int lim_min = g.ctx - g.n + t0 - g.j0 * 128; // the last key that every row of the unit sees, likewise
       float m_ref = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int t = 0; t < mine; ++t, ++n) {
@@ -502,10 +540,9 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           for (int c = 0; c < 128; c += 32) tmem_ld32(tS + c, xr + c);
           tmem_wait_ld();
         }
-        const int k0 = (g.j0 + t) * 128;
         const int gone = missing[(tile + t) & 7];
-        if (k0 + 127 > lim_min) {
-          const int last = lim - k0;
+        if (t * 128 + 127 > lim_min) {
+          const int last = lim - t * 128;
 #pragma unroll
           for (int c = 0; c < 128; ++c) x[c] = c <= last ? x[c] : -INFINITY;
         }
@@ -530,17 +567,17 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
             l2[0] = __fmul2_rn(l2[0], A);
             l2[1] = __fmul2_rn(l2[1], A);
 #pragma unroll
-            for (int c = 0; c < 128; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tO + c, o);
+            for (int c = 0; c < 128; c += 8) {            // a few columns at a time: the scores are live
+              uint32_t o[8];
+              tmem_ld8(tO + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
+              for (int k = 0; k < 8; k += 2) {
                 const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), A);
                 o[k] = __float_as_uint(v.x);
                 o[k + 1] = __float_as_uint(v.y);
               }
-              tmem_st16(tO + c, o);
+              tmem_st8(tO + c, o);
             }
           }
           m_ref = m_new;
@@ -548,16 +585,16 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         const float bias = kPShift - (m_ref == -INFINITY ? 0.f : m_ref);
         const float2 C2 = make_float2(C, C), B2 = make_float2(bias, bias);
 #pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          uint32_t p[32];
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t p[16];
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) {
+          for (int k = 0; k < 32; k += 2) {
             float2 e = __ffma2_rn(make_float2(x[c + k], x[c + k + 1]), C2, B2);
             e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
             p[k >> 1] = pack_half2(e.x, e.y);
           }
-          tmem_st32(tS + c / 2, p);
+          tmem_st16(tS + c / 2, p);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -565,7 +602,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         if (lane == 0) mbar_arrive(p_full + unit);
       }
       if (!ok) break;
-      tile += len;
+      tile += g.len;
       // ---- O of the segment ----
       const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       if (mine > 0) {
@@ -573,11 +610,14 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         ++n_o;
         tc_fence_after();
       }
-      const int TU = g.sq.T2 / 2, tok = t0 + row / group;
-      const bool real = row < TU * group && tok < g.sq.q.n;
-      const bool whole = g.j0 == 0 && g.j1 == g.nt;
-      float* part = a.prompt_part + static_cast<int64_t>(2 * blockIdx.x + (g.j0 > 0 ? 0 : 1)) * kPromptPartFloats;
-      const int64_t orow = static_cast<int64_t>(g.sq.q.q0 + tok) * a.Hq + g.h * group + row % group;
+      const uchar2 at = row_map[row];
+      const int tok = t0 + at.x;
+      const bool real = row < TU * group && tok < g.n;
+      const bool whole = g.whole;
+      float* part = a.prompt_part + static_cast<int64_t>(2 * blockIdx.x + (g.first ? 1 : 0)) * kPromptPartFloats;
+      const int64_t orow = static_cast<int64_t>(g.q0 + tok) * a.Hq + g.h * group + at.y;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
       const float f = l == 0.f ? 0.f : *a.c.v_ts / l;
 #pragma unroll
       for (int c = 0; c < 128; c += 32) {

@@ -1,8 +1,8 @@
 // Attention of many query rows per KV head over the 4-bit cache: prompts and chunks of prompts.
 //
-// Mathematics as in kv4_split.cuh (exact products of Q with K, FP32 scores, online softmax,
-// P = fp16(2^(s - m + 6)), FP32 O and l) on the 16-bit tensor cores of tcgen05. Q is taken as it is and K
-// decoded into Q's type, fp16 or bf16, exactly either way; V is decoded to fp16. The running maximum that P and O refer to follows the true one only when it
+// Mathematics as in kv4_split.cuh (Q to fp16 by a power of two per row, K and V decoded exactly to
+// fp16, FP32 scores, online softmax, P = fp16(2^(s - m + 6)), FP32 O and l) on the fp16 tensor cores of
+// tcgen05. The running maximum that P and O refer to follows the true one only when it
 // has risen by more than 2^8 (so P stays below 2^14): O in tensor memory is rarely rescaled.
 //
 // A work item is a KV head of a sequence and up to 256 query rows of it, rows being (token, head of
@@ -10,15 +10,17 @@
 // which share every decoded K and V tile of 128 keys. Bound: tensor cores and exponentials, 2048
 // cycles a tile each (16.8 MFLOP; 32768 exponentials at 16 a cycle), and next to them shared
 // memory: 3 x 64 KB read by the products and 64 KB written by the decoding, 2048 cycles at 128
-// bytes a cycle. P stays in tensor memory (as the A operand, over its own scores).
+// bytes a cycle. P stays in tensor memory (as the A operand).
 //
 // The key tiles of all items form one line, cut into equal ranges, one a CTA (kv4_range), whatever
 // the lengths and however few the rows; an item that crosses CTAs leaves partials.
 //
-// Roles (512 threads): warp 0 issues the products, warps 1-3 bring in Q, warps 4-7 decode K and V
-// pages from global memory (prefetched into registers a tile ahead) into the tensor cores'
+// Roles (512 threads): warp 0 issues Q K^T, warp 1 P V, warps 2-3 bring in Q, warps 4-7 decode K and
+// V pages from global memory (prefetched into registers a tile ahead) into the tensor cores'
 // 128-byte-swizzled layout, warps 8-11 and 12-15 are the units' softmax.
-// TMEM (512 columns): S_0, S_1 (P_u in the first 64 columns of S_u), O_0, O_1.
+// TMEM (512 columns): one S that the units use in turn, P_0, P_1, O_0, O_1. S is free as soon as its
+// softmax has it in registers, so the next scores are computed under the exponentials (with a
+// buffer for each unit and P in its place they would have to wait for the product with P).
 #pragma once
 #include "kv4_split.cuh"
 
@@ -69,20 +71,21 @@ struct PromptLayout {
   static constexpr int OFF_Q = 0;                        // [unit] 2 x 16 KB (64 channels each)
   static constexpr int OFF_K = 65536;                    // [stage] 2 x 16 KB (64 channels each)
   static constexpr int OFF_V = OFF_K + 65536;            // [stage] 2 x 16 KB (64 tokens each)
-  static constexpr int OFF_MAP = OFF_V + 65536;          // [128] a row's token and head within the unit
+  static constexpr int OFF_CODES = OFF_V + 65536;        // the next tile's codes and scales, K's and V's
+  static constexpr int OFF_MAP = OFF_CODES + 2 * 9216;   // [128] a row's token and head within the unit
   static constexpr int OFF_FLAG = OFF_MAP + 256;        // [8] pages missing, by tile
   static constexpr int OFF_RANGE = OFF_FLAG + 32;
   static constexpr int OFF_BAR = OFF_RANGE + (sizeof(Kv4Range) + 7) / 8 * 8;
   static constexpr int NSEG = 4;                         // segments handed out ahead
-  static constexpr int N_BARS = 17 + 2 * NSEG;
+  static constexpr int N_BARS = 20 + 2 * NSEG;
   static constexpr int OFF_SEG = (OFF_BAR + N_BARS * 8 + 16 + 15) / 16 * 16;
   static constexpr int SMEM_BYTES = OFF_SEG + NSEG * 64;
   static_assert(sizeof(PromptSeg) <= 64, "a segment's slot");
-  static constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
+  static constexpr int SMEM_ALLOC = SMEM_BYTES;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
-  static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1
+  static constexpr uint32_t T_S = 0, T_P = 128, T_O = 256;   // P_1 64 after P_0, O_1 128 after O_0
   static constexpr int THREADS = 512;
-  static constexpr int REGS_LAUNCH = 128, REGS_ISSUE = 80, REGS_DECODE = 80, REGS_SOFTMAX = 176;
+  static constexpr int REGS_LAUNCH = 128, REGS_ISSUE = 64, REGS_DECODE = 80, REGS_SOFTMAX = 184;
   static_assert(REGS_ISSUE + REGS_DECODE + 2 * REGS_SOFTMAX <= 4 * REGS_LAUNCH, "register split");
 };
 struct PromptWalk {
@@ -140,34 +143,40 @@ struct PromptWalk {
   }
 };
 
-// A block's scale times pairs of E2M1 values (as half2) in Q's type, exactly: in bf16 as
-// (value 2^-112) (scale 2^112), both and the product normal.
-template <typename T> struct KScale;
-template <> struct KScale<__half> {
-  __half2 f;
-  __device__ __forceinline__ explicit KScale(float s) : f(__float2half2_rn(s)) {}
-  __device__ __forceinline__ uint32_t times(uint32_t h) const { return hmul2(h, f); }
-};
-template <> struct KScale<__nv_bfloat16> {
-  __nv_bfloat162 f;
-  __device__ __forceinline__ explicit KScale(float s) : f(__float2bfloat162_rn(s * 0x1p112f)) {}
-  __device__ __forceinline__ uint32_t times(uint32_t h) const {
-    // the exponent field kept, fp16's bias of 15 read as bf16's of 127
-    const uint32_t b = ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-};
-// 16-byte asynchronous copy, or zeros.
-__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool copy) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
-               : "memory");
+// Largest magnitude of eight packed 16-bit values.
+template <typename T> __device__ __forceinline__ float amax8_packed(const uint4& u);
+template <> __device__ __forceinline__ float amax8_packed<__nv_bfloat16>(const uint4& u) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+  return fmaxf(__low2float(m), __high2float(m));
 }
+template <> __device__ __forceinline__ float amax8_packed<__half>(const uint4&) { return 0.f; }
+
+// A page id: a read-only load that stays where it is written, ahead of its use.
+__device__ __forceinline__ int prefetch_id(const int32_t* p) {
+  int v;
+  asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+// Asynchronous copy of 4, 8 or 16 bytes, or that many zeros.
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(void* dst, const void* src, bool copy) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(copy ? N : 0)
+                 : "memory");
+}
+
 template <typename T>
 __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   using L = PromptLayout;
-  extern __shared__ __align__(128) unsigned char kv4_smem[];
-  unsigned char* sm = kv4_smem + ((1024u - (smem_u32(kv4_smem) & 1023u)) & 1023u);
+  constexpr bool kConvertQ = std::is_same<T, __nv_bfloat16>::value;
+  // at a fixed, 1024-byte aligned address (there is no other shared memory): every address in it is a
+  // constant and takes no register
+  extern __shared__ __align__(1024) unsigned char kv4_prompt_smem[];
+  unsigned char* const sm = kv4_prompt_smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
   uint64_t* q_full = bars;                               // Q of the segment is in place
   uint64_t* q_empty = bars + 1;                          // its last QK^T is done
@@ -175,11 +184,13 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   uint64_t* k_empty = bars + 4;                          // [2]
   uint64_t* v_full = bars + 6;                           // [2]
   uint64_t* v_empty = bars + 8;                          // [2]
-  uint64_t* s_full = bars + 10;                          // [unit] scores ready; all PVs before them done
-  uint64_t* p_full = bars + 12;                          // [unit] P written, S read, O ready to add to
-  uint64_t* o_full = bars + 14;                          // [unit] the segment's last PV is done
-  uint64_t* mma_final = bars + 16;
-  uint64_t* seg_full = bars + 17;                        // [NSEG]
+  uint64_t* s_full = bars + 10;                          // [unit] S holds its scores
+  uint64_t* s_free = bars + 12;                          // S has been read (a phase per QK^T)
+  uint64_t* p_full = bars + 13;                          // [unit] P written, O ready to add to
+  uint64_t* pv_done = bars + 15;                         // [unit] P read, O added to
+  uint64_t* mma_final = bars + 17;                       // [2] QK issuer, PV issuer
+  uint64_t* q_raw = bars + 19;                           // Q has been copied in, to be converted
+  uint64_t* seg_full = bars + 20;                        // [NSEG]
   uint64_t* seg_empty = seg_full + L::NSEG;              // [NSEG]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -189,23 +200,29 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   const int group = a.Hq / a.c.Hkv;
 
   uchar2* row_map = reinterpret_cast<uchar2*>(sm + L::OFF_MAP);
+  if ((smem_u32(sm) & 1023u) != 0) {                     // cannot happen; the tensor cores would read other rows
+    if (threadIdx.x == 0) flag_error(kStatusBounds);
+    return;
+  }
   if (threadIdx.x < 128) row_map[threadIdx.x] = make_uchar2(threadIdx.x / group, threadIdx.x % group);
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 2);
+    mbar_init(q_raw, 2);
+    mbar_init(q_full, kConvertQ ? 8 : 2);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 4);
+      mbar_init(k_full + i, 2);
       mbar_init(k_empty + i, 1);
-      mbar_init(v_full + i, 4);
+      mbar_init(v_full + i, 2);
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
-      mbar_init(o_full + i, 1);
+      mbar_init(pv_done + i, 1);
+      mbar_init(mma_final + i, 1);
     }
-    mbar_init(mma_final, 1);
+    mbar_init(s_free, 4);
     for (int i = 0; i < L::NSEG; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 1 + 2 + 4 + 8);           // products, Q, decoding, softmax
+      mbar_init(seg_empty + i, 2 + 2 + 4 + 8);           // products, Q, decoding, softmax
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -229,121 +246,134 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     return *reinterpret_cast<const PromptSeg*>(sm + L::OFF_SEG + (seg % L::NSEG) * 64);
   };
   const int TU = 128 / group;                            // tokens of a unit
-  const uint32_t role = warp == 0 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
-  auto site = [&](uint64_t* bar, int tile) {
-    return wait_site(kKernelKv4Prompt, role, static_cast<uint32_t>(bar - bars), tile);
+  // A wait gives up when it has passed its limit, or when another one has (abort_flag: 1 + its barrier |
+  // role << 8); the place is reported at the end.
+  const int role = warp < 2 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
+  auto gave_up = [&](uint64_t* bar, long long t0) -> bool {
+    if (clock64() - t0 > kWaitLimitCycles) *abort_flag = 1 + static_cast<int>(bar - bars) + (role << 8);
+    return *abort_flag != 0;
   };
-  auto waitw = [&](uint64_t* bar, uint32_t parity, int tile) -> bool {
-    return bounded_wait_warp(bar, parity, abort_flag, site(bar, tile));
+  auto waitw = [&](uint64_t* bar, uint32_t parity) -> bool {        // by a whole warp
+    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+    while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+      if (__any_sync(0xffffffffu, gave_up(bar, t0))) return false;
+    return true;
+  };
+  auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {        // by one thread
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+      if (gave_up(bar, t0)) return false;
+    return true;
   };
 
   if (warp < 4) {
     setmaxnreg_to<L::REGS_ISSUE, L::REGS_LAUNCH>();
+    // descriptors of the first blocks: an offset of n bytes adds n / 16
     if (warp == 0) {
-      // ======================= products (one thread) =======================
+      // ======================= S = Q K^T (one thread) =======================
       if (lane == 0) {
-        auto wait1 = [&](uint64_t* bar, uint32_t parity, int tile) -> bool {
-          return bounded_wait(bar, parity, abort_flag, site(bar, tile));
-        };
-        constexpr uint32_t idesc_qk = idesc_f16(128, 128, std::is_same<T, __nv_bfloat16>::value);
-        constexpr uint32_t idesc_pv = idesc_f16(128, 128);
-        // descriptors of the first blocks; an offset of n bytes adds n / 16
+        constexpr uint32_t idesc = idesc_f16(128, 128);
         const uint64_t dQ = make_sdesc(smem_u32(sm + L::OFF_Q), 16, 1024, kSw128);
         const uint64_t dK = make_sdesc(smem_u32(sm + L::OFF_K), 16, 1024, kSw128);
-        const uint64_t dV = make_sdesc(smem_u32(sm + L::OFF_V), 16, 1024, kSw128);
-        auto qk = [&](int u, int tile) {                 // S_u = Q_u K^T
-          const uint64_t q = dQ + u * 2048, k = dK + (tile & 1) * 2048;
-          const uint32_t tS = tbase + L::T_S + u * 128;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
-          mma_commit(s_full + u);
-        };
-        auto pv = [&](int u, int tile, bool first) {     // O_u += P_u V
-          const uint64_t v = dV + (tile & 1) * 2048;
-          const uint32_t tS = tbase + L::T_S + u * 128, tO = tbase + L::T_O + u * 128;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ta(tO, tS + kk * 8, v + (kk >> 2) * 1024 + (kk & 3) * 2, idesc_pv, (first && kk == 0) ? 0u : 1u);
-        };
-        int tile = 0;
-        uint32_t odd = 0;                                // bit u: unit u's tiles so far, odd or even
+        int tile = 0, nq = 0;
         bool ok = true;
         for (int seg = 0;; ++seg) {
-          ok = wait1(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, tile);
+          ok = wait1(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1);
           if (!ok) break;
           const int len = seg_at(seg).len, mine0 = seg_at(seg).mine0, mine1 = seg_at(seg).mine1;
           const bool end = seg_at(seg).s < 0;
           mbar_arrive(seg_empty + seg % L::NSEG);
-          if (end) break;
-          ok = wait1(q_full, seg & 1, tile) && wait1(k_full + (tile & 1), (tile >> 1) & 1, tile);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int u = 0; u < 2; ++u)
-            if ((u ? mine1 : mine0) > 0) qk(u, tile);
-          mma_commit(k_empty + (tile & 1));
-          if (len == 1) mma_commit(q_empty);
+          if (end || !(ok = wait1(q_full, seg & 1))) break;
           for (int t = 0; t < len && ok; ++t, ++tile) {
-            bool v_in = false, k_in = false;
+            ok = wait1(k_full + (tile & 1), (tile >> 1) & 1);
+            const uint64_t k = dK + (tile & 1) * 2048;
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-              const int mine = u ? mine1 : mine0;
-              if (t < mine) {
-                ok = wait1(p_full + u, (odd >> u) & 1, tile) &&
-                     (v_in || wait1(v_full + (tile & 1), (tile >> 1) & 1, tile));
-                if (!ok) break;
-                v_in = true;
-                tc_fence_after();
-                pv(u, tile, t == 0);
-                odd ^= 1u << u;
-                if (t + 1 == mine) mma_commit(o_full + u);
-              }
-              if (t + 1 < mine) {
-                ok = k_in || wait1(k_full + ((tile + 1) & 1), ((tile + 1) >> 1) & 1, tile);
-                if (!ok) break;
-                k_in = true;
-                tc_fence_after();
-                qk(u, tile + 1);
-              }
+            for (int u = 0; u < 2 && ok; ++u) {
+              if (t >= (u ? mine1 : mine0)) continue;
+              if (nq > 0 && !(ok = wait1(s_free, (nq - 1) & 1))) break;
+              tc_fence_after();
+              const uint64_t q = dQ + u * 2048;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_f16(tbase + L::T_S, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
+              mma_commit(s_full + u);
+              ++nq;
             }
-            if (!ok) break;
-            if (t + 1 < len) mma_commit(k_empty + ((tile + 1) & 1));
-            if (t + 2 == len) mma_commit(q_empty);
-            mma_commit(v_empty + (tile & 1));
+            mma_commit(k_empty + (tile & 1));
           }
           if (!ok) break;
+          mma_commit(q_empty);
         }
         mma_commit(mma_final);
         mbar_wait(mma_final, 0);
       }
       __syncwarp();
-    } else if (warp == 3) {
-      // ============================ segments (one thread) ============================
+    } else if (warp == 1) {
+      // ======================= O += P V (one thread) =======================
       if (lane == 0) {
-        PromptWalk walk;
-        walk.start(a, rng);
-        bool more = true;
-        for (int seg = 0; more; ++seg) {
-          if (seg >= L::NSEG && !bounded_wait(seg_empty + seg % L::NSEG, (seg / L::NSEG - 1) & 1, abort_flag,
-                                              site(seg_empty + seg % L::NSEG, seg)))
-            break;
-          PromptSeg g;
-          more = walk.next(a, g);
-          if (!more) g.s = -1;
-          *reinterpret_cast<PromptSeg*>(sm + L::OFF_SEG + (seg % L::NSEG) * 64) = g;
-          mbar_arrive(seg_full + seg % L::NSEG);
+        constexpr uint32_t idesc = idesc_f16(128, 128);
+        const uint64_t dV = make_sdesc(smem_u32(sm + L::OFF_V), 16, 1024, kSw128);
+        int tile = 0;
+        uint32_t odd = 0;                                // bit u: unit u's tiles so far, odd or even
+        bool ok = true;
+        for (int seg = 0;; ++seg) {
+          ok = wait1(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1);
+          if (!ok) break;
+          const int len = seg_at(seg).len, mine0 = seg_at(seg).mine0, mine1 = seg_at(seg).mine1;
+          const bool end = seg_at(seg).s < 0;
+          mbar_arrive(seg_empty + seg % L::NSEG);
+          if (end) break;
+          for (int t = 0; t < len && ok; ++t, ++tile) {
+            ok = wait1(v_full + (tile & 1), (tile >> 1) & 1);
+            const uint64_t v = dV + (tile & 1) * 2048;
+#pragma unroll 1
+            for (int u = 0; u < 2 && ok; ++u) {
+              if (t >= (u ? mine1 : mine0)) continue;
+              if (!(ok = wait1(p_full + u, (odd >> u) & 1))) break;
+              odd ^= 1u << u;
+              tc_fence_after();
+              const uint32_t tP = tbase + L::T_P + u * 64, tO = tbase + L::T_O + u * 128;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_f16_ta(tO, tP + kk * 8, v + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, (t == 0 && kk == 0) ? 0u : 1u);
+              mma_commit(pv_done + u);
+            }
+            mma_commit(v_empty + (tile & 1));
+          }
+          if (!ok) break;
         }
+        mma_commit(mma_final + 1);
+        mbar_wait(mma_final + 1, 0);
       }
       __syncwarp();
     } else {
-      // ================================ Q ================================
+      // ================================ segments and Q ================================
+      // One thread hands out the segments, two ahead of the one whose Q is brought in (its slot's last
+      // user is done by then: see the wait for q_empty).
+      PromptWalk walk;
+      int handed = 0;
+      auto hand_out = [&]() {
+        PromptSeg g;
+        if (!walk.next(a, g)) g.s = -1;
+        *reinterpret_cast<PromptSeg*>(sm + L::OFF_SEG + (handed % L::NSEG) * 64) = g;
+        mbar_arrive(seg_full + handed % L::NSEG);
+        ++handed;
+      };
+      if (warp == 3 && lane == 0) {
+        walk.start(a, rng);
+        hand_out();
+        hand_out();
+      }
+      __syncwarp();
       // Copied as it is, half a warp a row, 16 bytes a thread; rows without a token are zero. The
-      // eights of channels are stored in K's order (see the decoding).
+      // eights of channels are stored in K's order (see the decoding). (bf16: the softmax warps make
+      // it fp16 in place.)
       const int hw = lane >> 4, ch = lane & 15;
-      const int pos = ((ch & 8) << 11) | (((ch & 7) ^ ((ch & 8) >> 2)) << 4);
+      const int pos = ((ch & 8) << 11) | (((ch & 7) ^ ((ch & 8) >> 1)) << 4);
       for (int seg = 0;; ++seg) {
-        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, seg)) break;
+        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1)) break;
         const PromptSeg& g = seg_at(seg);
         if (g.s < 0) break;
         const int left = g.n - g.tok;                    // tokens from the item's first on
@@ -351,188 +381,260 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
         // the last segment's products have read Q
-        if (seg > 0 && !waitw(q_empty, (seg - 1) & 1, seg)) break;
+        if (seg > 0 && !waitw(q_empty, (seg - 1) & 1)) break;
+        if (warp == 3 && lane == 0 &&
+            (handed < L::NSEG || wait1(seg_empty + handed % L::NSEG, (handed / L::NSEG - 1) & 1)))
+          hand_out();
+        __syncwarp();
 #pragma unroll 4
-        for (int r = (warp - 1) * 2 + hw; r < 256; r += 4) {
+        for (int r = (warp - 2) * 2 + hw; r < 256; r += 4) {
           const int ru = r & 127;
           const uchar2 at = row_map[ru];
           const int tok = (r >> 7) * TU + at.x;
           const bool real = ru < TU * group && tok < left;
-          cp_async16_or_zero(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4)),
-                             real ? q + tok * a.q_stride + at.y * kKv4D : q, real);
+          cp_async_or_zero<16>(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4)),
+                               real ? q + tok * a.q_stride + at.y * kKv4D : q, real);
         }
         cp_async_commit();
         cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        if (lane == 0) mbar_arrive(kConvertQ ? q_raw : q_full);
       }
     }
   } else if (warp < 8) {
     setmaxnreg_to<L::REGS_DECODE, L::REGS_LAUNCH>();
     // ============================ K and V decoding ============================
-    // K: thread (token row, quarter of the channels): four words of eight channels become four
-    // 16-byte chunks. Of the upper 64 channels, chunks 2 c and 2 c + 1 trade places with
-    // 2 (c ^ 1) and 2 (c ^ 1) + 1, so that the eight threads of two rows write eight different
-    // 16-byte banks; Q has the same order.
-    // V: thread (page, eight tokens, 16 channels): four token pairs of a channel are a chunk.
-    const int tid = threadIdx.x - 128;
-    const int kr = tid >> 2, kq = tid & 3;
-    const int vp = tid >> 6, vt = tid & 7, vb = (tid >> 3) & 7;
-    bool ok = true;
-    int tile = 0;
-    // prefetched: the next tile's page ids, its K and (after K) its V
-    uint4 kc[4], vc[4];
-    uint32_t ks[4];
-    uint2 vs;
-    int v_left;                                          // this thread's V slots that lie in the context
-    // the tile at hand, and the next one's segment and place
-    int id0 = -1, id1 = -1, h = 0, ctx = 0, j = 0;
-    int seg = -1, jn = 0, j_end = 0;
-    // steps to the next tile: its page ids; false when there is none
-    auto next_tile = [&](int& p0, int& p1) -> bool {
-      if (++jn >= j_end) {
+    // Warps 4 and 5 decode K, warps 6 and 7 V, tile by tile and in four pieces a tile. Codes and scales
+    // come a tile ahead, by asynchronous copies that each thread makes for itself: a piece that it has
+    // decoded it replaces by the same one of the next tile, whose page ids it has read a tile before that.
+    // (Loops over the pieces stay loops: with all roles unrolled the code of a tile passes the
+    // instruction cache, and a decoded word cost five times its instructions.)
+    const int tid = threadIdx.x & 63;
+    struct Place {                                       // of a tile: its pages (-1: none), KV head, slots in the context
+      int id0, id1, h, left;
+    };
+    int seg = -1, j = 0, j_end = 0;
+    auto next_tile = [&](Place& t) -> bool {
+      if (++j >= j_end) {
         if (seg >= 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
         }
         ++seg;
-        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, tile) || seg_at(seg).s < 0) return false;
-        jn = seg_at(seg).j0;
-        j_end = jn + seg_at(seg).len;
+        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1) || seg_at(seg).s < 0) return false;
+        j = seg_at(seg).j0;
+        j_end = j + seg_at(seg).len;
       }
-      // the second page may lie behind the context: the first again then, with no slot that counts
-      const int32_t* row = a.table + static_cast<int64_t>(seg_at(seg).s) * a.max_pages;
-      const int np = (seg_at(seg).ctx + 63) >> 6;
-      p0 = __ldg(row + 2 * jn);
-      p1 = __ldg(row + min(2 * jn + 1, np - 1));
+      const PromptSeg& g = seg_at(seg);
+      const int32_t* row = a.table + static_cast<int64_t>(g.s) * a.max_pages + 2 * j;
+      t.h = g.h;
+      t.left = g.ctx - j * 128;
+      t.id0 = prefetch_id(row);
+      t.id1 = -1;
+      if (t.left > 64) t.id1 = prefetch_id(row + 1);
       return true;
     };
-    auto valid = [&](int id) { return id >= 0 && id < a.c.num_pages; };
-    auto load_k = [&]() {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int id = i < 2 ? id0 : id1, row = (i & 1) * 32 + kr;
-        kc[i] = make_uint4(0, 0, 0, 0);
-        ks[i] = 0;
-        if (valid(id)) {
-          const int64_t tok = (static_cast<int64_t>(id) * a.c.Hkv + h) * 64 + row;
-          kc[i] = __ldg(reinterpret_cast<const uint4*>(a.c.k_pages + tok * 64 + kq * 16));
-          ks[i] = __ldg(reinterpret_cast<const uint16_t*>(a.c.k_scales + tok * 8 + kq * 2));
+    auto valid = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.num_pages); };
+    // tiles now (being decoded), next (being loaded), third (its ids being read); the pipeline fills
+    // in two rounds without a tile, -2 and -1
+    Place now, next, third;
+    bool more = false, after = false;
+    if (warp < 6) {
+      // K: a thread has half the channels of rows kr + 32 i: eight words of eight channels become eight
+      // 16-byte chunks. Of the upper half, chunks c and c ^ 4 trade places, so that the eight threads of
+      // four rows write to eight different banks of 16 bytes; Q has the same order.
+      const int kr = tid >> 1, kh = tid & 1;
+      const int kpos = ((kh * 4) ^ (kr & 7)) << 4;       // of a word's chunk in its row, but for the word
+      unsigned char* codes = sm + L::OFF_CODES + tid * 16;          // [piece][2][64] 16 bytes
+      unsigned char* scales = sm + L::OFF_CODES + 8192 + tid * 4;   // [piece][64] 4 bytes
+      auto load = [&](int i, const Place& t, bool any) {
+        const int id = i < 2 ? t.id0 : t.id1;
+        const bool good = any && valid(id);
+        const int64_t head = good ? static_cast<int64_t>(id) * a.c.Hkv + t.h : 0;
+        const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32 + (i & 1) * 2048;
+        cp_async_or_zero<16>(codes + i * 2048, k, good);
+        cp_async_or_zero<16>(codes + i * 2048 + 1024, k + 16, good);
+        cp_async_or_zero<4>(scales + i * 256, a.c.k_scales + head * 512 + kr * 8 + kh * 4 + (i & 1) * 256, good);
+        cp_async_commit();
+      };
+      for (int tile = -2;; ++tile) {
+        const int stg = tile & 1;
+        const bool far = (after || tile == -2) && next_tile(third);
+        if (tile >= 2 && !waitw(k_empty + stg, ((tile >> 1) - 1) & 1)) break;
+        if (tid == 0 && more) {
+          const int gone = (valid(now.id0) ? 0 : 1) | (now.left <= 64 || valid(now.id1) ? 0 : 2);
+          missing[tile & 7] = gone;
+          if (gone) flag_error(kStatusBounds);
         }
-      }
-    };
-    auto load_v = [&]() {
-      const int id = vp ? id1 : id0;
+        unsigned char* row = sm + L::OFF_K + stg * 32768 + kh * 16384 + kr * 128;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i, row += 4096) {
+          if (more) {
+          cp_async_wait<3>();
+          const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + i * 256);
+          const __half2 s01 = e4m3x2_to_half2(sc & 0xFFFFu), s23 = e4m3x2_to_half2(sc >> 16);
+          __half2 f0 = __low2half2(s01), f1 = __high2half2(s01);
+#pragma unroll 1
+          for (int o = 0; o < 2; ++o) {
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 2048 + o * 1024);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vc[i] = make_uint4(0, 0, 0, 0);
-      vs = make_uint2(0, 0);
-      if (valid(id)) {
-        const int64_t head = static_cast<int64_t>(id) * a.c.Hkv + h;
+            for (int e = 0; e < 4; ++e) {
+              uint32_t d[4];
+              e2m1x8_to_half2(w[e], d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vc[i] = __ldg(reinterpret_cast<const uint4*>(a.c.v_pages + (head * 32 + vt * 4 + i) * 128 + vb * 16));
-        vs = __ldg(reinterpret_cast<const uint2*>(a.c.v_scales + (head * 8 + vb) * 64 + vt * 8));
-      }
-      v_left = ctx - (j * 128 + vp * 64 + vt * 8);
-    };
-    int n0 = -1, n1 = -1;                                // page ids of the tile after
-    bool more = next_tile(id0, id1);
-    if (more) {
-      h = seg_at(seg).h; ctx = seg_at(seg).ctx; j = jn;
-      load_k();
-    }
-    while (more && ok) {
-      const int stg = tile & 1;
-      const bool after = next_tile(n0, n1);
-      // ---- K ----
-      if (tile >= 2 && !waitw(k_empty + stg, ((tile >> 1) - 1) & 1, tile)) { ok = false; break; }
-      load_v();
-      if (tid == 0) {
-        const int gone = (valid(id0) ? 0 : 1) | (valid(id1) ? 0 : 2);
-        missing[tile & 7] = gone;
-        if (gone) flag_error(kStatusBounds);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 32 + kr;
-        const __half2 sc = e4m3x2_to_half2(ks[i]);
-        const KScale<T> f0(__low2float(sc)), f1(__high2float(sc));
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&kc[i]);
-        unsigned char* row = sm + L::OFF_K + stg * 32768 + (kq >> 1) * 16384 + r * 128;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t d[4];
-          e2m1x8_to_half2(w[e], d);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) d[x] = e < 2 ? f0.times(d[x]) : f1.times(d[x]);
-          const int chunk = ((kq & 1) * 4 + (e ^ (kq & 2))) ^ (r & 7);
-          *reinterpret_cast<uint4*>(row + chunk * 16) = make_uint4(d[0], d[1], d[2], d[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(k_full + stg);
-      // ---- V, with the next tile's K on its way ----
-      id0 = n0; id1 = n1;
-      if (after) {
-        h = seg_at(seg).h; ctx = seg_at(seg).ctx; j = jn;
-        load_k();
-      }
-      if (tile >= 2 && !waitw(v_empty + stg, ((tile >> 1) - 1) & 1, tile)) { ok = false; break; }
-      {
-        if (v_left < 8) {                                // slots behind it: value 0 (weight 0 x NaN is not 0)
-          const uint64_t keep = v_left <= 0 ? 0 : (1ull << (8 * v_left)) - 1;
-          vs.x &= static_cast<uint32_t>(keep);
-          vs.y &= static_cast<uint32_t>(keep >> 32);
-        }
-        const __half2 f[4] = {e4m3x2_to_half2(vs.x & 0xFFFFu), e4m3x2_to_half2(vs.x >> 16),
-                              e4m3x2_to_half2(vs.y & 0xFFFFu), e4m3x2_to_half2(vs.y >> 16)};
-        unsigned char* base = sm + L::OFF_V + stg * 32768 + vp * 16384 + vb * 16 * 128;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t d[4][4];                              // [token pair][channel]
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e2m1x8_to_half2(reinterpret_cast<const uint32_t*>(&vc[i])[e], d[i]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) d[i][x] = hmul2(d[i][x], f[i]);
+              for (int x = 0; x < 4; ++x) d[x] = hmul2(d[x], e < 2 ? f0 : f1);
+              *reinterpret_cast<uint4*>(row + (kpos ^ ((o * 4 + e) << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
+            }
+            f0 = __low2half2(s23);
+            f1 = __high2half2(s23);
           }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int cc = e * 4 + x;
-            *reinterpret_cast<uint4*>(base + cc * 128 + ((vt ^ (cc & 7)) << 4)) = make_uint4(d[0][x], d[1][x], d[2][x], d[3][x]);
           }
+          if (tile > -2) load(i, next, after);
         }
+        if (more) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full + stg);
+        }
+        now = next;
+        next = third;
+        more = after;
+        after = far;
+        if (!more && !after) break;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_full + stg);
-      more = after;
-      ++tile;
+    } else {
+      // V: a thread has eight tokens of 16 channels of each page, a piece being eight of the channels:
+      // four token pairs of a channel are a chunk.
+      const int vt = tid & 7, vb = tid >> 3;
+      unsigned char* codes = sm + L::OFF_CODES + 9216 + tid * 8;    // [piece][token pair][64] 8 bytes
+      unsigned char* scales = sm + L::OFF_CODES + 9216 + 8192 + tid * 8;   // [page][64] 8 bytes
+      auto load = [&](int i, const Place& t, bool any) {
+        const int id = i < 2 ? t.id0 : t.id1;
+        const bool good = any && valid(id);
+        const int64_t head = good ? static_cast<int64_t>(id) * a.c.Hkv + t.h : 0;
+        const uint8_t* v = a.c.v_pages + head * 4096 + vt * 512 + vb * 16 + (i & 1) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cp_async_or_zero<8>(codes + i * 2048 + k * 512, v + k * 128, good);
+        if (i & 1) cp_async_or_zero<8>(scales + (i >> 1) * 512, a.c.v_scales + head * 512 + vb * 64 + vt * 8, good);
+        cp_async_commit();
+      };
+      for (int tile = -2;; ++tile) {
+        const int stg = tile & 1;
+        const bool far = (after || tile == -2) && next_tile(third);
+        if (tile >= 2 && !waitw(v_empty + stg, ((tile >> 1) - 1) & 1)) break;
+        unsigned char* row = sm + L::OFF_V + stg * 32768 + vb * 16 * 128;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i, row += (i & 1) ? 1024 : 16384 - 1024) {
+          if (more) {
+          // a page's scales come with its second piece: the first waits for both
+          if (i & 1) cp_async_wait<3>(); else cp_async_wait<2>();
+          uint2 sc = *reinterpret_cast<const uint2*>(scales + (i >> 1) * 512);
+          const int left = now.left - (i >> 1) * 64 - vt * 8;   // of the thread's slots, those in the context
+          if (left < 8) {                                // the others: value 0 (weight 0 x NaN is not 0)
+            const uint64_t keep = left <= 0 ? 0 : (1ull << (8 * left)) - 1;
+            sc.x &= static_cast<uint32_t>(keep);
+            sc.y &= static_cast<uint32_t>(keep >> 32);
+          }
+          const __half2 f[4] = {e4m3x2_to_half2(sc.x & 0xFFFFu), e4m3x2_to_half2(sc.x >> 16),
+                                e4m3x2_to_half2(sc.y & 0xFFFFu), e4m3x2_to_half2(sc.y >> 16)};
+          uint2 c[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const uint2*>(codes + i * 2048 + k * 512);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t d[4][4];                            // [token pair][channel 4 e + x of the piece]
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              e2m1x8_to_half2(e ? c[k].y : c[k].x, d[k]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) d[k][x] = hmul2(d[k][x], f[k]);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(row + (4 * e + x) * 128 + ((vt ^ (4 * e + x)) << 4)) =
+                  make_uint4(d[0][x], d[1][x], d[2][x], d[3][x]);
+          }
+          }
+          if (tile > -2) load(i, next, after);
+        }
+        if (more) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full + stg);
+        }
+        now = next;
+        next = third;
+        more = after;
+        after = far;
+        if (!more && !after) break;
+      }
     }
   } else {
     setmaxnreg_to<L::REGS_SOFTMAX, L::REGS_LAUNCH>();
     // ================================ softmax ================================
     const int wq = warp & 3, unit = (warp - 8) >> 2, row = wq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tbase + L::T_S + unit * 128 + lane_addr, tO = tbase + L::T_O + unit * 128 + lane_addr;
-    const float C = *a.c.k_ts * a.softmax_scale * kLog2e;
+    const uint32_t tS = tbase + L::T_S + lane_addr, tP = tbase + L::T_P + unit * 64 + lane_addr;
+    const uint32_t tO = tbase + L::T_O + unit * 128 + lane_addr;
     bool ok = true;
-    int tile = 0, n = 0, n_o = 0;                        // tiles; of this unit; segments with any
+    int tile = 0, n = 0;                                 // tiles; of this unit
     for (int seg = 0;; ++seg) {
-      if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1, tile)) break;
+      if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1)) break;
       const PromptSeg& g = seg_at(seg);
       if (g.s < 0) break;
       const int mine = unit == 0 ? g.mine0 : g.mine1;
       const int t0 = g.tok + unit * TU;
+      float C = *a.c.k_ts * a.softmax_scale * kLog2e;
+      if constexpr (kConvertQ) {
+        // the thread's row of Q to fp16 under a power of two (kv4_row_factor), which goes into its C
+        if (!waitw(q_raw, seg & 1)) break;
+        unsigned char* q = sm + L::OFF_Q + unit * 32768 + row * 128;
+        float m = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c)
+          m = fmaxf(m, amax8_packed<T>(*reinterpret_cast<const uint4*>(q + (c >> 3) * 16384 + (((c ^ row) & 7) << 4))));
+        const float2 fac = kv4_row_factor<T>(m), f2 = make_float2(fac.x, fac.x);
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * 16384 + (((c ^ row) & 7) << 4));
+          uint4 u = *at;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __fmul2_rn(to_float2<T>(w[e]), f2);
+            w[e] = pack_half2(f.x, f.y);
+          }
+          *at = u;
+        }
+        C *= fac.y;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
       const int lim = g.ctx - g.n + t0 + row_map[row].x - g.j0 * 128;   // the last key seen, from the segment's first
       const int lim_min = g.ctx - g.n + t0 - g.j0 * 128; // the last key that every row of the unit sees, likewise
       float m_ref = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int t = 0; t < mine; ++t, ++n) {
-        if (!waitw(s_full + unit, n & 1, n)) { ok = false; break; }
+        if (!waitw(s_full + unit, n & 1)) { ok = false; break; }
         tc_fence_after();
+        const int gone = missing[(tile + t) & 7];
+        if (t * 128 + 127 > lim_min || gone != 0) {      // keys that not every row sees: masked in place
+          const int last = lim - t * 128;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t y[16];
+            tmem_ld16(tS + c, y);
+            tmem_wait_ld();
+            const int end = (gone & (c < 64 ? 1 : 2)) ? -1 : last - c;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] = k <= end ? y[k] : 0xFF800000u;
+            tmem_st16(tS + c, y);
+          }
+          tmem_wait_st();
+        }
         float x[128];
         {
           uint32_t* xr = reinterpret_cast<uint32_t*>(x);
@@ -540,17 +642,9 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           for (int c = 0; c < 128; c += 32) tmem_ld32(tS + c, xr + c);
           tmem_wait_ld();
         }
-        const int gone = missing[(tile + t) & 7];
-        if (t * 128 + 127 > lim_min) {
-          const int last = lim - t * 128;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = c <= last ? x[c] : -INFINITY;
-        }
-        if (gone) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (gone & (c < 64 ? 1 : 2)) x[c] = -INFINITY;
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 128; c += 8) {
@@ -559,43 +653,44 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         }
         const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * C;
         // a row's first keys, or a rise past the limit: the reference follows
-        if (__any_sync(0xffffffffu, mt > m_ref + kRiseLimit)) {
-          const float m_new = fmaxf(m_ref, mt);
-          if (t > 0) {
-            const float al = m_new == -INFINITY ? 1.f : ex2_approx(m_ref - m_new);
-            const float2 A = make_float2(al, al);
-            l2[0] = __fmul2_rn(l2[0], A);
-            l2[1] = __fmul2_rn(l2[1], A);
-#pragma unroll
-            for (int c = 0; c < 128; c += 8) {            // a few columns at a time: the scores are live
-              uint32_t o[8];
-              tmem_ld8(tO + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 8; k += 2) {
-                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), A);
-                o[k] = __float_as_uint(v.x);
-                o[k + 1] = __float_as_uint(v.y);
-              }
-              tmem_st8(tO + c, o);
-            }
-          }
-          m_ref = m_new;
-        }
+        const bool rise = __any_sync(0xffffffffu, mt > m_ref + kRiseLimit);
+        const float m_old = m_ref;
+        if (rise) m_ref = fmaxf(m_ref, mt);
         const float bias = kPShift - (m_ref == -INFINITY ? 0.f : m_ref);
         const float2 C2 = make_float2(C, C), B2 = make_float2(bias, bias);
+        const float al = m_ref == -INFINITY ? 1.f : ex2_approx(m_old - m_ref);
+        const float2 A = make_float2(al, al);
+        l2[0] = __fmul2_rn(l2[0], A);
+        l2[1] = __fmul2_rn(l2[1], A);
+        // P packed, in eights of registers that the scores leave free one after another
+        uint32_t p[8][8];
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float2 e = __ffma2_rn(make_float2(x[c + k], x[c + k + 1]), C2, B2);
-            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
-            p[k >> 1] = pack_half2(e.x, e.y);
-          }
-          tmem_st16(tS + c / 2, p);
+        for (int k = 0; k < 128; k += 2) {
+          float2 e = __ffma2_rn(make_float2(x[k], x[k + 1]), C2, B2);
+          e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+          l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
+          p[k >> 4][(k >> 1) & 7] = pack_half2(e.x, e.y);
         }
+        // the unit's last product has read P and is in O
+        if (n > 0 && !waitw(pv_done + unit, (n - 1) & 1)) { ok = false; break; }
+        if (rise && t > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), A);
+              o[k] = __float_as_uint(v.x);
+              o[k + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(tO + c, o);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tmem_st8(tP + 8 * k, p[k]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -606,20 +701,23 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       // ---- O of the segment ----
       const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       if (mine > 0) {
-        if (!waitw(o_full + unit, n_o & 1, n)) { ok = false; break; }
-        ++n_o;
+        if (!waitw(pv_done + unit, (n - 1) & 1)) { ok = false; break; }
         tc_fence_after();
       }
-      const uchar2 at = row_map[row];
-      const int tok = t0 + at.x;
-      const bool real = row < TU * group && tok < g.n;
+      // (thread's place read afresh: addresses computed from it before the tiles would stay in registers)
+      int me;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(me));
+      const int my_row = me & 127, my_unit = (me >> 7) & 1;
+      const uchar2 at = row_map[my_row];
+      const int tok = g.tok + my_unit * TU + at.x;
+      const bool real = my_row < TU * group && tok < g.n;
       const bool whole = g.whole;
       float* part = a.prompt_part + static_cast<int64_t>(2 * blockIdx.x + (g.first ? 1 : 0)) * kPromptPartFloats;
       const int64_t orow = static_cast<int64_t>(g.q0 + tok) * a.Hq + g.h * group + at.y;
       __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
       const float f = l == 0.f ? 0.f : *a.c.v_ts / l;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t o[32];
         if (mine > 0) {
@@ -629,8 +727,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0;
         }
-        if (!real) continue;
-        if (whole) {
+        if (real && whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * kKv4D + c);
 #pragma unroll
           for (int k = 0; k < 32; k += 8)
@@ -638,16 +735,17 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
                                      pack2<T>(__uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f),
                                      pack2<T>(__uint_as_float(o[k + 4]) * f, __uint_as_float(o[k + 5]) * f),
                                      pack2<T>(__uint_as_float(o[k + 6]) * f, __uint_as_float(o[k + 7]) * f));
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(part + (unit * 128 + row) * kKv4D + c);
+        } else if (real) {
+          uint4* dst = reinterpret_cast<uint4*>(part + (my_unit * 128 + my_row) * kKv4D + c);
 #pragma unroll
           for (int k = 0; k < 32; k += 4) dst[k >> 2] = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
+        __syncwarp();
       }
       if (real) {
         if (!whole) {
-          part[256 * kKv4D + unit * 128 + row] = m_ref;
-          part[256 * (kKv4D + 1) + unit * 128 + row] = l;
+          part[256 * kKv4D + my_unit * 128 + my_row] = m_ref;
+          part[256 * (kKv4D + 1) + my_unit * 128 + my_row] = l;
         } else if (a.lse != nullptr) {
           a.lse[orow] = l == 0.f ? -INFINITY : (m_ref + log2f(l) - kPShift) * kLn2;
         }
@@ -660,6 +758,10 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag != 0) {
+    flag_error(kStatusTimeout);
+    record_timeout(wait_site(kKernelKv4Prompt, *abort_flag >> 8, (*abort_flag & 0xFF) - 1, 0));
   }
 }
 

@@ -77,16 +77,15 @@ struct PromptLayout {
   static constexpr int OFF_RANGE = OFF_FLAG + 32;
   static constexpr int OFF_BAR = OFF_RANGE + (sizeof(Kv4Range) + 7) / 8 * 8;
   static constexpr int NSEG = 4;                         // segments handed out ahead
-  static constexpr int N_BARS = 20 + 2 * NSEG;
+  static constexpr int N_BARS = 18 + 2 * NSEG;
   static constexpr int OFF_SEG = (OFF_BAR + N_BARS * 8 + 16 + 15) / 16 * 16;
-  static constexpr int SMEM_BYTES = OFF_SEG + NSEG * 64;
+  static constexpr int OFF_WALK = OFF_SEG + NSEG * 64;
+  static constexpr int SMEM_BYTES = OFF_WALK + 64;
   static_assert(sizeof(PromptSeg) <= 64, "a segment's slot");
   static constexpr int SMEM_ALLOC = SMEM_BYTES;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
-  static constexpr uint32_t T_S = 0, T_P = 128, T_O = 256;   // P_1 64 after P_0, O_1 128 after O_0
+  static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1
   static constexpr int THREADS = 512;
-  static constexpr int REGS_LAUNCH = 128, REGS_ISSUE = 64, REGS_DECODE = 80, REGS_SOFTMAX = 184;
-  static_assert(REGS_ISSUE + REGS_DECODE + 2 * REGS_SOFTMAX <= 4 * REGS_LAUNCH, "register split");
 };
 struct PromptWalk {
   PromptSeq sq;
@@ -158,15 +157,13 @@ __device__ __forceinline__ int prefetch_id(const int32_t* p) {
   asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
-// Asynchronous copy of 4, 8 or 16 bytes, or that many zeros.
-template <int N>
-__device__ __forceinline__ void cp_async_or_zero(void* dst, const void* src, bool copy) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(copy ? N : 0)
-                 : "memory");
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// 16-byte asynchronous copy, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
+               : "memory");
 }
 
 template <typename T>
@@ -184,13 +181,12 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   uint64_t* k_empty = bars + 4;                          // [2]
   uint64_t* v_full = bars + 6;                           // [2]
   uint64_t* v_empty = bars + 8;                          // [2]
-  uint64_t* s_full = bars + 10;                          // [unit] S holds its scores
-  uint64_t* s_free = bars + 12;                          // S has been read (a phase per QK^T)
-  uint64_t* p_full = bars + 13;                          // [unit] P written, O ready to add to
-  uint64_t* pv_done = bars + 15;                         // [unit] P read, O added to
-  uint64_t* mma_final = bars + 17;                       // [2] QK issuer, PV issuer
-  uint64_t* q_raw = bars + 19;                           // Q has been copied in, to be converted
-  uint64_t* seg_full = bars + 20;                        // [NSEG]
+  uint64_t* s_full = bars + 10;                          // [unit] scores ready; all products before them done
+  uint64_t* p_full = bars + 12;                          // [unit] P written over its scores, O ready to add to
+  uint64_t* o_full = bars + 14;                          // [unit] the segment's last product with P is done
+  uint64_t* mma_final = bars + 16;
+  uint64_t* q_raw = bars + 17;                           // Q has been copied in, to be converted
+  uint64_t* seg_full = bars + 18;                        // [NSEG]
   uint64_t* seg_empty = seg_full + L::NSEG;              // [NSEG]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -216,13 +212,12 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
-      mbar_init(pv_done + i, 1);
-      mbar_init(mma_final + i, 1);
+      mbar_init(o_full + i, 1);
     }
-    mbar_init(s_free, 4);
+    mbar_init(mma_final, 1);
     for (int i = 0; i < L::NSEG; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 2 + 2 + 4 + 8);           // products, Q, decoding, softmax
+      mbar_init(seg_empty + i, 1 + 2 + 4 + 8);           // products, Q, decoding, softmax
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -241,14 +236,14 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       },
       a.S, 2, a.prompt_plan, rng);
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // (uniform for the compiler too)
   auto seg_at = [&](int seg) -> const PromptSeg& {
     return *reinterpret_cast<const PromptSeg*>(sm + L::OFF_SEG + (seg % L::NSEG) * 64);
   };
   const int TU = 128 / group;                            // tokens of a unit
   // A wait gives up when it has passed its limit, or when another one has (abort_flag: 1 + its barrier |
   // role << 8); the place is reported at the end.
-  const int role = warp < 2 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
+  const int role = warp == 0 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
   auto gave_up = [&](uint64_t* bar, long long t0) -> bool {
     if (clock64() - t0 > kWaitLimitCycles) *abort_flag = 1 + static_cast<int>(bar - bars) + (role << 8);
     return *abort_flag != 0;
@@ -269,100 +264,94 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   };
 
   if (warp < 4) {
-    setmaxnreg_to<L::REGS_ISSUE, L::REGS_LAUNCH>();
-    // descriptors of the first blocks: an offset of n bytes adds n / 16
     if (warp == 0) {
-      // ======================= S = Q K^T (one thread) =======================
-      if (lane == 0) {
+      // ======================= products =======================
+      {
         constexpr uint32_t idesc = idesc_f16(128, 128);
+        // descriptors of the first blocks: an offset of n bytes adds n / 16
         const uint64_t dQ = make_sdesc(smem_u32(sm + L::OFF_Q), 16, 1024, kSw128);
         const uint64_t dK = make_sdesc(smem_u32(sm + L::OFF_K), 16, 1024, kSw128);
-        int tile = 0, nq = 0;
-        bool ok = true;
-        for (int seg = 0;; ++seg) {
-          ok = wait1(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1);
-          if (!ok) break;
-          const int len = seg_at(seg).len, mine0 = seg_at(seg).mine0, mine1 = seg_at(seg).mine1;
-          const bool end = seg_at(seg).s < 0;
-          mbar_arrive(seg_empty + seg % L::NSEG);
-          if (end || !(ok = wait1(q_full, seg & 1))) break;
-          for (int t = 0; t < len && ok; ++t, ++tile) {
-            ok = wait1(k_full + (tile & 1), (tile >> 1) & 1);
-            const uint64_t k = dK + (tile & 1) * 2048;
-#pragma unroll 1
-            for (int u = 0; u < 2 && ok; ++u) {
-              if (t >= (u ? mine1 : mine0)) continue;
-              if (nq > 0 && !(ok = wait1(s_free, (nq - 1) & 1))) break;
-              tc_fence_after();
-              const uint64_t q = dQ + u * 2048;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_f16(tbase + L::T_S, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
-              mma_commit(s_full + u);
-              ++nq;
-            }
-            mma_commit(k_empty + (tile & 1));
-          }
-          if (!ok) break;
-          mma_commit(q_empty);
-        }
-        mma_commit(mma_final);
-        mbar_wait(mma_final, 0);
-      }
-      __syncwarp();
-    } else if (warp == 1) {
-      // ======================= O += P V (one thread) =======================
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_f16(128, 128);
         const uint64_t dV = make_sdesc(smem_u32(sm + L::OFF_V), 16, 1024, kSw128);
+        auto qk = [&](int u, int tile) {                 // S_u = Q_u K^T
+          const uint64_t q = dQ + u * 2048, k = dK + (tile & 1) * 2048;
+          const uint32_t tS = tbase + L::T_S + u * 128;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_elect(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
+          mma_commit_elect(s_full + u);
+        };
         int tile = 0;
         uint32_t odd = 0;                                // bit u: unit u's tiles so far, odd or even
         bool ok = true;
         for (int seg = 0;; ++seg) {
-          ok = wait1(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1);
+          ok = waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1);
           if (!ok) break;
-          const int len = seg_at(seg).len, mine0 = seg_at(seg).mine0, mine1 = seg_at(seg).mine1;
-          const bool end = seg_at(seg).s < 0;
-          mbar_arrive(seg_empty + seg % L::NSEG);
-          if (end) break;
-          for (int t = 0; t < len && ok; ++t, ++tile) {
-            ok = wait1(v_full + (tile & 1), (tile >> 1) & 1);
-            const uint64_t v = dV + (tile & 1) * 2048;
+          const int len = __shfl_sync(0xffffffffu, seg_at(seg).len, 0);
+          const int mine0 = __shfl_sync(0xffffffffu, seg_at(seg).mine0, 0);
+          const int mine1 = __shfl_sync(0xffffffffu, seg_at(seg).mine1, 0);
+          const bool end = __shfl_sync(0xffffffffu, seg_at(seg).s, 0) < 0;
+          if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
+          __syncwarp();
+          if (end || !(ok = waitw(q_full, seg & 1))) break;
+          // round -1: the first scores; round t: unit by unit, tile t's product with V and tile t + 1's scores
+          for (int t = -1; t < len && ok; ++t) {
+            bool v_in = false, k_in = false;
 #pragma unroll 1
-            for (int u = 0; u < 2 && ok; ++u) {
-              if (t >= (u ? mine1 : mine0)) continue;
-              if (!(ok = wait1(p_full + u, (odd >> u) & 1))) break;
-              odd ^= 1u << u;
-              tc_fence_after();
-              const uint32_t tP = tbase + L::T_P + u * 64, tO = tbase + L::T_O + u * 128;
+            for (int u = 0; u < 2; ++u) {
+              const int mine = u ? mine1 : mine0;
+              if (t >= 0 && t < mine) {
+                ok = waitw(p_full + u, (odd >> u) & 1) && (v_in || waitw(v_full + (tile & 1), (tile >> 1) & 1));
+                if (!ok) break;
+                v_in = true;
+                odd ^= 1u << u;
+                tc_fence_after();
+                const uint64_t v = dV + (tile & 1) * 2048;
+                const uint32_t tP = tbase + L::T_S + u * 128, tO = tbase + L::T_O + u * 128;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_f16_ta(tO, tP + kk * 8, v + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, (t == 0 && kk == 0) ? 0u : 1u);
-              mma_commit(pv_done + u);
+                for (int kk = 0; kk < 8; ++kk)           // O_u += P_u V
+                  mma_f16_ta_elect(tO, tP + kk * 8, v + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, (t == 0 && kk == 0) ? 0u : 1u);
+                if (t + 1 == mine) mma_commit_elect(o_full + u);
+              }
+              if (t + 1 < mine) {
+                const int nx = t < 0 ? tile : tile + 1;
+                ok = k_in || waitw(k_full + (nx & 1), (nx >> 1) & 1);
+                if (!ok) break;
+                k_in = true;
+                tc_fence_after();
+                qk(u, nx);
+              }
             }
-            mma_commit(v_empty + (tile & 1));
+            if (!ok) break;
+            if (t + 1 < len) mma_commit_elect(k_empty + ((t < 0 ? tile : tile + 1) & 1));
+            if (t + 2 == len) mma_commit_elect(q_empty);
+            if (t >= 0) {
+              mma_commit_elect(v_empty + (tile & 1));
+              ++tile;
+            }
           }
           if (!ok) break;
         }
-        mma_commit(mma_final + 1);
-        mbar_wait(mma_final + 1, 0);
+        mma_commit_elect(mma_final);
+        mbar_wait(mma_final, 0);
+        __syncwarp();
       }
       __syncwarp();
+    } else if (warp == 1) {
+      // (its registers serve the others of the warpgroup)
     } else {
       // ================================ segments and Q ================================
       // One thread hands out the segments, two ahead of the one whose Q is brought in (its slot's last
       // user is done by then: see the wait for q_empty).
-      PromptWalk walk;
+      PromptWalk* const walk = reinterpret_cast<PromptWalk*>(sm + L::OFF_WALK);   // (no registers for it)
       int handed = 0;
       auto hand_out = [&]() {
-        PromptSeg g;
-        if (!walk.next(a, g)) g.s = -1;
-        *reinterpret_cast<PromptSeg*>(sm + L::OFF_SEG + (handed % L::NSEG) * 64) = g;
+        PromptSeg* g = reinterpret_cast<PromptSeg*>(sm + L::OFF_SEG + (handed % L::NSEG) * 64);
+        if (!walk->next(a, *g)) g->s = -1;
         mbar_arrive(seg_full + handed % L::NSEG);
         ++handed;
       };
       if (warp == 3 && lane == 0) {
-        walk.start(a, rng);
+        walk->start(a, rng);
         hand_out();
         hand_out();
       }
@@ -386,13 +375,13 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
             (handed < L::NSEG || wait1(seg_empty + handed % L::NSEG, (handed / L::NSEG - 1) & 1)))
           hand_out();
         __syncwarp();
-#pragma unroll 4
+#pragma unroll 2
         for (int r = (warp - 2) * 2 + hw; r < 256; r += 4) {
           const int ru = r & 127;
           const uchar2 at = row_map[ru];
           const int tok = (r >> 7) * TU + at.x;
           const bool real = ru < TU * group && tok < left;
-          cp_async_or_zero<16>(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4)),
+          cp_async16_or_zero(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4)),
                                real ? q + tok * a.q_stride + at.y * kKv4D : q, real);
         }
         cp_async_commit();
@@ -403,64 +392,60 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       }
     }
   } else if (warp < 8) {
-    setmaxnreg_to<L::REGS_DECODE, L::REGS_LAUNCH>();
     // ============================ K and V decoding ============================
-    // Warps 4 and 5 decode K, warps 6 and 7 V, tile by tile and in four pieces a tile. Codes and scales
-    // come a tile ahead, by asynchronous copies that each thread makes for itself: a piece that it has
-    // decoded it replaces by the same one of the next tile, whose page ids it has read a tile before that.
-    // (Loops over the pieces stay loops: with all roles unrolled the code of a tile passes the
+    // Warps 4 and 5 decode K, warps 6 and 7 V, tile by tile. Codes and scales come a tile ahead, by
+    // asynchronous copies that each thread makes for itself: a page's part that it has decoded it replaces
+    // by the same one of the next tile, whose page ids it has read a tile before that. A page that
+    // does not exist leaves what was there (codes are always finite) and counts with scale 0.
+    // (Loops over the pages stay loops: with all roles unrolled the code of a tile passes the
     // instruction cache, and a decoded word cost five times its instructions.)
     const int tid = threadIdx.x & 63;
     struct Place {                                       // of a tile: its pages (-1: none), KV head, slots in the context
       int id0, id1, h, left;
     };
-    int seg = -1, j = 0, j_end = 0;
-    auto next_tile = [&](Place& t) -> bool {
-      if (++j >= j_end) {
+    int seg = -1, tiles = 0, seg_h = 0, left = 0;
+    const int32_t* ids = nullptr;
+    auto next_tile = [&](int& id0, int& id1) -> bool {
+      if (--tiles < 0) {
         if (seg >= 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
         }
         ++seg;
-        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1) || seg_at(seg).s < 0) return false;
-        j = seg_at(seg).j0;
-        j_end = j + seg_at(seg).len;
+        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1) || seg_at(seg).s < 0) {
+          tiles = 0;
+          return false;
+        }
+        const PromptSeg& g = seg_at(seg);
+        tiles = g.len - 1;
+        seg_h = g.h;
+        left = g.ctx - g.j0 * 128;
+        ids = a.table + static_cast<int64_t>(g.s) * a.max_pages + 2 * g.j0;
       }
-      const PromptSeg& g = seg_at(seg);
-      const int32_t* row = a.table + static_cast<int64_t>(g.s) * a.max_pages + 2 * j;
-      t.h = g.h;
-      t.left = g.ctx - j * 128;
-      t.id0 = prefetch_id(row);
-      t.id1 = -1;
-      if (t.left > 64) t.id1 = prefetch_id(row + 1);
+      id0 = prefetch_id(ids);
+      id1 = -1;
+      if (left > 64) id1 = prefetch_id(ids + 1);
+      left -= 128;
+      ids += 2;
       return true;
     };
     auto valid = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.num_pages); };
     // tiles now (being decoded), next (being loaded), third (its ids being read); the pipeline fills
     // in two rounds without a tile, -2 and -1
-    Place now, next, third;
+    Place now = {-1, -1, 0, 0}, next = now;
+    int third0 = -1, third1 = -1;
     bool more = false, after = false;
     if (warp < 6) {
-      // K: a thread has half the channels of rows kr + 32 i: eight words of eight channels become eight
-      // 16-byte chunks. Of the upper half, chunks c and c ^ 4 trade places, so that the eight threads of
-      // four rows write to eight different banks of 16 bytes; Q has the same order.
+      // K: a thread has half the channels of rows kr and kr + 32 of a page: a row's eight words of eight channels
+      // become eight 16-byte chunks. Of the upper half, chunks c and c ^ 4 trade places, so that the eight
+      // threads of four rows write to eight different banks of 16 bytes; Q has the same order.
       const int kr = tid >> 1, kh = tid & 1;
-      const int kpos = ((kh * 4) ^ (kr & 7)) << 4;       // of a word's chunk in its row, but for the word
-      unsigned char* codes = sm + L::OFF_CODES + tid * 16;          // [piece][2][64] 16 bytes
-      unsigned char* scales = sm + L::OFF_CODES + 8192 + tid * 4;   // [piece][64] 4 bytes
-      auto load = [&](int i, const Place& t, bool any) {
-        const int id = i < 2 ? t.id0 : t.id1;
-        const bool good = any && valid(id);
-        const int64_t head = good ? static_cast<int64_t>(id) * a.c.Hkv + t.h : 0;
-        const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32 + (i & 1) * 2048;
-        cp_async_or_zero<16>(codes + i * 2048, k, good);
-        cp_async_or_zero<16>(codes + i * 2048 + 1024, k + 16, good);
-        cp_async_or_zero<4>(scales + i * 256, a.c.k_scales + head * 512 + kr * 8 + kh * 4 + (i & 1) * 256, good);
-        cp_async_commit();
-      };
+      const uint32_t kpos = static_cast<uint32_t>(((kh * 4) ^ (kr & 7)) << 4);   // a word's chunk in its row, but for the word
+      unsigned char* codes = sm + L::OFF_CODES + tid * 16;          // [page][row][2][64] 16 bytes
+      unsigned char* scales = sm + L::OFF_CODES + 8192 + tid * 4;   // [page][row][64] 4 bytes
       for (int tile = -2;; ++tile) {
         const int stg = tile & 1;
-        const bool far = (after || tile == -2) && next_tile(third);
+        const bool far = (after || tile == -2) && next_tile(third0, third1);
         if (tile >= 2 && !waitw(k_empty + stg, ((tile >> 1) - 1) & 1)) break;
         if (tid == 0 && more) {
           const int gone = (valid(now.id0) ? 0 : 1) | (now.left <= 64 || valid(now.id1) ? 0 : 2);
@@ -469,29 +454,41 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         }
         unsigned char* row = sm + L::OFF_K + stg * 32768 + kh * 16384 + kr * 128;
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i, row += 4096) {
+        for (int it = 0; it < 8; ++it) {                 // page it / 4, row kr + 32 (it / 2 % 2), four words
+          const int pg = it >> 2;
           if (more) {
-          cp_async_wait<3>();
-          const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + i * 256);
-          const __half2 s01 = e4m3x2_to_half2(sc & 0xFFFFu), s23 = e4m3x2_to_half2(sc >> 16);
-          __half2 f0 = __low2half2(s01), f1 = __high2half2(s01);
-#pragma unroll 1
-          for (int o = 0; o < 2; ++o) {
-            const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 2048 + o * 1024);
+            if ((it & 3) == 0) cp_async_wait<1>();
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + (it >> 1) * 256 + (it & 1) * 2);
+            const __half2 s2 = e4m3x2_to_half2(valid(pg ? now.id1 : now.id0) ? sc : 0u);
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + it * 1024);
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
+            unsigned char* dst = row + (it >> 1) * 4096;
+            const uint32_t pos = kpos ^ ((it & 1) << 6);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+              const __half2 f = e < 2 ? __low2half2(s2) : __high2half2(s2);
               uint32_t d[4];
               e2m1x8_to_half2(w[e], d);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) d[x] = hmul2(d[x], e < 2 ? f0 : f1);
-              *reinterpret_cast<uint4*>(row + (kpos ^ ((o * 4 + e) << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
+              for (int x = 0; x < 4; ++x) d[x] = hmul2(d[x], f);
+              *reinterpret_cast<uint4*>(dst + (pos ^ (e << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
             }
-            f0 = __low2half2(s23);
-            f1 = __high2half2(s23);
           }
+          if ((it & 3) == 3) {
+            const int id = pg ? next.id1 : next.id0;
+            if (after && valid(id)) {
+              const int64_t head = static_cast<int64_t>(id) * a.c.Hkv + next.h;
+              const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32;
+              const uint8_t* s = a.c.k_scales + head * 512 + kr * 8 + kh * 4;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                cp_async16(codes + pg * 4096 + i * 2048, k + i * 2048);
+                cp_async16(codes + pg * 4096 + i * 2048 + 1024, k + i * 2048 + 16);
+                cp_async4(scales + pg * 512 + i * 256, s + i * 256, true);
+              }
+            }
+            cp_async_commit();
           }
-          if (tile > -2) load(i, next, after);
         }
         if (more) {
           fence_proxy_async_smem();
@@ -499,65 +496,59 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           if (lane == 0) mbar_arrive(k_full + stg);
         }
         now = next;
-        next = third;
+        next = Place{third0, third1, seg_h, left + 128};   // (the walk has not moved since)
         more = after;
         after = far;
         if (!more && !after) break;
       }
     } else {
-      // V: a thread has eight tokens of 16 channels of each page, a piece being eight of the channels:
-      // four token pairs of a channel are a chunk.
+      // V: a thread has eight tokens of 16 channels of each page: four token pairs of a channel are a chunk.
       const int vt = tid & 7, vb = tid >> 3;
-      unsigned char* codes = sm + L::OFF_CODES + 9216 + tid * 8;    // [piece][token pair][64] 8 bytes
+      unsigned char* codes = sm + L::OFF_CODES + 9216 + tid * 16;          // [page][token pair][64] 16 bytes
       unsigned char* scales = sm + L::OFF_CODES + 9216 + 8192 + tid * 8;   // [page][64] 8 bytes
-      auto load = [&](int i, const Place& t, bool any) {
-        const int id = i < 2 ? t.id0 : t.id1;
-        const bool good = any && valid(id);
-        const int64_t head = good ? static_cast<int64_t>(id) * a.c.Hkv + t.h : 0;
-        const uint8_t* v = a.c.v_pages + head * 4096 + vt * 512 + vb * 16 + (i & 1) * 8;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cp_async_or_zero<8>(codes + i * 2048 + k * 512, v + k * 128, good);
-        if (i & 1) cp_async_or_zero<8>(scales + (i >> 1) * 512, a.c.v_scales + head * 512 + vb * 64 + vt * 8, good);
-        cp_async_commit();
-      };
       for (int tile = -2;; ++tile) {
         const int stg = tile & 1;
-        const bool far = (after || tile == -2) && next_tile(third);
+        const bool far = (after || tile == -2) && next_tile(third0, third1);
         if (tile >= 2 && !waitw(v_empty + stg, ((tile >> 1) - 1) & 1)) break;
         unsigned char* row = sm + L::OFF_V + stg * 32768 + vb * 16 * 128;
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i, row += (i & 1) ? 1024 : 16384 - 1024) {
+        for (int pg = 0; pg < 2; ++pg, row += 16384) {
           if (more) {
-          // a page's scales come with its second piece: the first waits for both
-          if (i & 1) cp_async_wait<3>(); else cp_async_wait<2>();
-          uint2 sc = *reinterpret_cast<const uint2*>(scales + (i >> 1) * 512);
-          const int left = now.left - (i >> 1) * 64 - vt * 8;   // of the thread's slots, those in the context
-          if (left < 8) {                                // the others: value 0 (weight 0 x NaN is not 0)
-            const uint64_t keep = left <= 0 ? 0 : (1ull << (8 * left)) - 1;
-            sc.x &= static_cast<uint32_t>(keep);
-            sc.y &= static_cast<uint32_t>(keep >> 32);
-          }
-          const __half2 f[4] = {e4m3x2_to_half2(sc.x & 0xFFFFu), e4m3x2_to_half2(sc.x >> 16),
-                                e4m3x2_to_half2(sc.y & 0xFFFFu), e4m3x2_to_half2(sc.y >> 16)};
-          uint2 c[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const uint2*>(codes + i * 2048 + k * 512);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t d[4][4];                            // [token pair][channel 4 e + x of the piece]
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e2m1x8_to_half2(e ? c[k].y : c[k].x, d[k]);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) d[k][x] = hmul2(d[k][x], f[k]);
+            cp_async_wait<1>();
+            uint2 sc = *reinterpret_cast<const uint2*>(scales + pg * 512);
+            const int in = valid(pg ? now.id1 : now.id0) ? now.left - pg * 64 - vt * 8 : 0;   // slots in the context
+            if (in < 8) {                                // the others: value 0 (weight 0 x NaN is not 0)
+              const uint64_t keep = in <= 0 ? 0 : (1ull << (8 * in)) - 1;
+              sc.x &= static_cast<uint32_t>(keep);
+              sc.y &= static_cast<uint32_t>(keep >> 32);
             }
+            const __half2 f[4] = {e4m3x2_to_half2(sc.x & 0xFFFFu), e4m3x2_to_half2(sc.x >> 16),
+                                  e4m3x2_to_half2(sc.y & 0xFFFFu), e4m3x2_to_half2(sc.y >> 16)};
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+              uint32_t d[4][4];                          // [token pair][channel 4 e + x]
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4*>(row + (4 * e + x) * 128 + ((vt ^ (4 * e + x)) << 4)) =
-                  make_uint4(d[0][x], d[1][x], d[2][x], d[3][x]);
+              for (int k = 0; k < 4; ++k) {
+                e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(codes + pg * 4096 + k * 1024 + e * 4), d[k]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) d[k][x] = hmul2(d[k][x], f[k]);
+              }
+              unsigned char* dst = row + e * 512;
+              const uint32_t pos = static_cast<uint32_t>(vt ^ ((e & 1) * 4)) << 4;
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(dst + x * 128 + (pos ^ (x << 4))) = make_uint4(d[0][x], d[1][x], d[2][x], d[3][x]);
+            }
           }
+          const int id = pg ? next.id1 : next.id0;
+          if (after && valid(id)) {
+            const int64_t head = static_cast<int64_t>(id) * a.c.Hkv + next.h;
+            const uint8_t* v = a.c.v_pages + head * 4096 + vt * 512 + vb * 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) cp_async16(codes + pg * 4096 + k * 1024, v + k * 128);
+            cp_async8(scales + pg * 512, a.c.v_scales + head * 512 + vb * 64 + vt * 8);
           }
-          if (tile > -2) load(i, next, after);
+          cp_async_commit();
         }
         if (more) {
           fence_proxy_async_smem();
@@ -565,21 +556,19 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           if (lane == 0) mbar_arrive(v_full + stg);
         }
         now = next;
-        next = third;
+        next = Place{third0, third1, seg_h, left + 128};   // (the walk has not moved since)
         more = after;
         after = far;
         if (!more && !after) break;
       }
     }
   } else {
-    setmaxnreg_to<L::REGS_SOFTMAX, L::REGS_LAUNCH>();
     // ================================ softmax ================================
     const int wq = warp & 3, unit = (warp - 8) >> 2, row = wq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tbase + L::T_S + lane_addr, tP = tbase + L::T_P + unit * 64 + lane_addr;
-    const uint32_t tO = tbase + L::T_O + unit * 128 + lane_addr;
+    const uint32_t tS = tbase + L::T_S + unit * 128 + lane_addr, tO = tbase + L::T_O + unit * 128 + lane_addr;
     bool ok = true;
-    int tile = 0, n = 0;                                 // tiles; of this unit
+    int tile = 0, n = 0, n_o = 0;                        // tiles; of this unit; segments with any
     for (int seg = 0;; ++seg) {
       if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1)) break;
       const PromptSeg& g = seg_at(seg);
@@ -613,8 +602,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
-      const int lim = g.ctx - g.n + t0 + row_map[row].x - g.j0 * 128;   // the last key seen, from the segment's first
-      const int lim_min = g.ctx - g.n + t0 - g.j0 * 128; // the last key that every row of the unit sees, likewise
+      const int lim_min = g.ctx - g.n + t0 - g.j0 * 128; // the last key that every row of the unit sees, from the segment's first
       float m_ref = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int t = 0; t < mine; ++t, ++n) {
@@ -622,7 +610,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         tc_fence_after();
         const int gone = missing[(tile + t) & 7];
         if (t * 128 + 127 > lim_min || gone != 0) {      // keys that not every row sees: masked in place
-          const int last = lim - t * 128;
+          const int last = lim_min + row_map[row].x - t * 128;
 #pragma unroll 1
           for (int c = 0; c < 128; c += 16) {
             uint32_t y[16];
@@ -635,62 +623,62 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           }
           tmem_wait_st();
         }
-        float x[128];
-        {
-          uint32_t* xr = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) tmem_ld32(tS + c, xr + c);
-          tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], x[c + 2 * k], x[c + 2 * k + 1]);
-        }
-        const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * C;
-        // a row's first keys, or a rise past the limit: the reference follows
-        const bool rise = __any_sync(0xffffffffu, mt > m_ref + kRiseLimit);
-        const float m_old = m_ref;
-        if (rise) m_ref = fmaxf(m_ref, mt);
-        const float bias = kPShift - (m_ref == -INFINITY ? 0.f : m_ref);
-        const float2 C2 = make_float2(C, C), B2 = make_float2(bias, bias);
-        const float al = m_ref == -INFINITY ? 1.f : ex2_approx(m_old - m_ref);
-        const float2 A = make_float2(al, al);
-        l2[0] = __fmul2_rn(l2[0], A);
-        l2[1] = __fmul2_rn(l2[1], A);
-        // P packed, in eights of registers that the scores leave free one after another
-        uint32_t p[8][8];
-#pragma unroll
-        for (int k = 0; k < 128; k += 2) {
-          float2 e = __ffma2_rn(make_float2(x[k], x[k + 1]), C2, B2);
-          e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-          l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
-          p[k >> 4][(k >> 1) & 7] = pack_half2(e.x, e.y);
-        }
-        // the unit's last product has read P and is in O
-        if (n > 0 && !waitw(pv_done + unit, (n - 1) & 1)) { ok = false; break; }
-        if (rise && t > 0) {
-          tc_fence_after();
+        // the scores are read twice, 32 columns at a time: the maximum, then the weights, which take
+        // the place of scores already read (all 128 in registers would cost the code of 128, which,
+        // with the other roles', passes the instruction cache)
+        float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_wait_ld();
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t y[32];
+          tmem_ld32(tS + c, y);
+          tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), A);
-              o[k] = __float_as_uint(v.x);
-              o[k + 1] = __float_as_uint(v.y);
-            }
-            tmem_st32(tO + c, o);
+          for (int k = 0; k < 32; k += 4) {
+            m2[0] = fmax3(m2[0], __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+            m2[1] = fmax3(m2[1], __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
           }
         }
+        const float mt = fmaxf(m2[0], m2[1]) * C;
+        // a row's first keys, or a rise past the limit: the reference follows
+        if (__any_sync(0xffffffffu, mt > m_ref + kRiseLimit)) {
+          const float m_new = fmaxf(m_ref, mt);
+          if (t > 0) {
+            const float al = m_new == -INFINITY ? 1.f : ex2_approx(m_ref - m_new);
+            const float2 A = make_float2(al, al);
+            l2[0] = __fmul2_rn(l2[0], A);
+            l2[1] = __fmul2_rn(l2[1], A);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) tmem_st8(tP + 8 * k, p[k]);
+              for (int k = 0; k < 32; k += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), A);
+                o[k] = __float_as_uint(v.x);
+                o[k + 1] = __float_as_uint(v.y);
+              }
+              tmem_st32(tO + c, o);
+            }
+          }
+          m_ref = m_new;
+        }
+        const float bias = kPShift - (m_ref == -INFINITY ? 0.f : m_ref);
+        const float2 C2 = make_float2(C, C), B2 = make_float2(bias, bias);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t y[32], p[16];
+          tmem_ld32(tS + c, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), C2, B2);
+            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
+            p[k >> 1] = pack_half2(e.x, e.y);
+          }
+          tmem_st16(tS + c / 2, p);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -701,7 +689,8 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       // ---- O of the segment ----
       const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       if (mine > 0) {
-        if (!waitw(pv_done + unit, (n - 1) & 1)) { ok = false; break; }
+        if (!waitw(o_full + unit, n_o & 1)) { ok = false; break; }
+        ++n_o;
         tc_fence_after();
       }
       // (thread's place read afresh: addresses computed from it before the tiles would stay in registers)

@@ -922,15 +922,8 @@ qk4v8_status launch_kv4_split(const Kv4AttnArgs& a, int ctas, cudaStream_t strea
 template <typename T>
 qk4v8_status launch_kv4_prompt(const Kv4AttnArgs& a, int ctas, cudaStream_t stream) {
   using L = PromptLayout;
-  // as for the other prefill kernels: the launch's register count has to be the one that the
-  // setmaxnreg split is computed from
   static PerDeviceOnce opt_in;
-  if (!opt_in.run(current_device(), [] {
-        cudaFuncAttributes fa;
-        return set_smem(kv4_prompt_kernel<T>, L::SMEM_ALLOC) &&
-               cudaFuncGetAttributes(&fa, kv4_prompt_kernel<T>) == cudaSuccess && fa.numRegs == L::REGS_LAUNCH;
-      }))
-    return QK4V8_ERR_CUDA;
+  if (!opt_in.run(current_device(), [] { return set_smem(kv4_prompt_kernel<T>, L::SMEM_ALLOC); })) return QK4V8_ERR_CUDA;
   kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_ALLOC, stream>>>(a);
   if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
   if (ctas > 1) kv4_prompt_merge_kernel<T><<<dim3(ctas - 1, 8), 256, 0, stream>>>(a);

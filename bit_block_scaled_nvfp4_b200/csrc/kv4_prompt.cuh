@@ -623,17 +623,18 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           }
           tmem_wait_st();
         }
-        // the scores are read twice, 32 columns at a time: the maximum, then the weights, which take
+        // the scores are read twice, piece by piece: the maximum, then the weights, which take
         // the place of scores already read (all 128 in registers would cost the code of 128, which,
         // with the other roles', passes the instruction cache)
         float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t y[32];
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t y[64];
           tmem_ld32(tS + c, y);
+          tmem_ld32(tS + c + 32, y + 32);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
+          for (int k = 0; k < 64; k += 4) {
             m2[0] = fmax3(m2[0], __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
             m2[1] = fmax3(m2[1], __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
           }
@@ -665,11 +666,15 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         }
         const float bias = kPShift - (m_ref == -INFINITY ? 0.f : m_ref);
         const float2 C2 = make_float2(C, C), B2 = make_float2(bias, bias);
+        uint32_t z[32];
+        tmem_ld32(tS, z);
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           uint32_t y[32], p[16];
-          tmem_ld32(tS + c, y);
           tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[k] = z[k];
+          if (c < 96) tmem_ld32(tS + c + 32, z);         // the next ones under these
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
             float2 e = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), C2, B2);

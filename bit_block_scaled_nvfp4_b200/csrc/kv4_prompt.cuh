@@ -77,14 +77,14 @@ struct PromptLayout {
   static constexpr int OFF_RANGE = OFF_FLAG + 32;
   static constexpr int OFF_BAR = OFF_RANGE + (sizeof(Kv4Range) + 7) / 8 * 8;
   static constexpr int NSEG = 4;                         // segments handed out ahead
-  static constexpr int N_BARS = 18 + 2 * NSEG;
+  static constexpr int N_BARS = 24 + 2 * NSEG;
   static constexpr int OFF_SEG = (OFF_BAR + N_BARS * 8 + 16 + 15) / 16 * 16;
   static constexpr int OFF_WALK = OFF_SEG + NSEG * 64;
   static constexpr int SMEM_BYTES = OFF_WALK + 64;
   static_assert(sizeof(PromptSeg) <= 64, "a segment's slot");
   static constexpr int SMEM_ALLOC = SMEM_BYTES;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
-  static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1
+  static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1; S + 64 for a tile's second half
   static constexpr int THREADS = 512;
 };
 struct PromptWalk {
@@ -181,12 +181,14 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   uint64_t* k_empty = bars + 4;                          // [2]
   uint64_t* v_full = bars + 6;                           // [2]
   uint64_t* v_empty = bars + 8;                          // [2]
-  uint64_t* s_full = bars + 10;                          // [unit] scores ready; all products before them done
-  uint64_t* p_full = bars + 12;                          // [unit] P written over its scores, O ready to add to
-  uint64_t* o_full = bars + 14;                          // [unit] the segment's last product with P is done
-  uint64_t* mma_final = bars + 16;
-  uint64_t* q_raw = bars + 17;                           // Q has been copied in, to be converted
-  uint64_t* seg_full = bars + 18;                        // [NSEG]
+  uint64_t* s_full = bars + 10;                          // [unit][half tile] its scores are ready
+  uint64_t* p_full = bars + 14;                          // [unit][half tile] P written over its scores
+  uint64_t* pv_done = bars + 18;                         // [unit][half tile] its product with V is done
+  // (Barriers for each half: a softmax may be two halves ahead of the products, and nobody may wait two
+  // phases behind. It is never further ahead: a half's scores are issued after its last product.)
+  uint64_t* mma_final = bars + 22;
+  uint64_t* q_raw = bars + 23;                           // Q has been copied in, to be converted
+  uint64_t* seg_full = bars + 24;                        // [NSEG]
   uint64_t* seg_empty = seg_full + L::NSEG;              // [NSEG]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -210,9 +212,12 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 2);
       mbar_init(v_empty + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
-      mbar_init(o_full + i, 1);
+      mbar_init(s_full + 2 * i, 1);
+      mbar_init(s_full + 2 * i + 1, 1);
+      mbar_init(p_full + 2 * i, 4);
+      mbar_init(p_full + 2 * i + 1, 4);
+      mbar_init(pv_done + 2 * i, 1);
+      mbar_init(pv_done + 2 * i + 1, 1);
     }
     mbar_init(mma_final, 1);
     for (int i = 0; i < L::NSEG; ++i) {
@@ -267,19 +272,11 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     if (warp == 0) {
       // ======================= products =======================
       {
-        constexpr uint32_t idesc = idesc_f16(128, 128);
+        constexpr uint32_t idesc_qk = idesc_f16(128, 64), idesc_pv = idesc_f16(128, 128);
         // descriptors of the first blocks: an offset of n bytes adds n / 16
         const uint64_t dQ = make_sdesc(smem_u32(sm + L::OFF_Q), 16, 1024, kSw128);
         const uint64_t dK = make_sdesc(smem_u32(sm + L::OFF_K), 16, 1024, kSw128);
         const uint64_t dV = make_sdesc(smem_u32(sm + L::OFF_V), 16, 1024, kSw128);
-        auto qk = [&](int u, int tile) {                 // S_u = Q_u K^T
-          const uint64_t q = dQ + u * 2048, k = dK + (tile & 1) * 2048;
-          const uint32_t tS = tbase + L::T_S + u * 128;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_elect(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
-          mma_commit_elect(s_full + u);
-        };
         int tile = 0;
         uint32_t odd = 0;                                // bit u: unit u's tiles so far, odd or even
         bool ok = true;
@@ -293,43 +290,46 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
           __syncwarp();
           if (end || !(ok = waitw(q_full, seg & 1))) break;
-          // round -1: the first scores; round t: unit by unit, tile t's product with V and tile t + 1's scores
-          for (int t = -1; t < len && ok; ++t) {
-            bool v_in = false, k_in = false;
+          // x counts half tiles. Rounds -2 and -1: the first tile's scores. Round x, unit by unit: the product of
+          // half x with V, and the scores of half x + 2 in its place.
+#pragma unroll 1
+          for (int x = -2; x < 2 * len && ok; ++x) {
+            const int h = x & 1, now = tile + (x >> 1), nx = now + 1;     // tiles of halves x and x + 2
+            if (x + 2 < 2 * len && h == 0 && !(ok = waitw(k_full + (nx & 1), (nx >> 1) & 1))) break;
+            if (x >= 0 && h == 0 && !(ok = waitw(v_full + (now & 1), (now >> 1) & 1))) break;
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-              const int mine = u ? mine1 : mine0;
-              if (t >= 0 && t < mine) {
-                ok = waitw(p_full + u, (odd >> u) & 1) && (v_in || waitw(v_full + (tile & 1), (tile >> 1) & 1));
-                if (!ok) break;
-                v_in = true;
-                odd ^= 1u << u;
+              const int mine = 2 * (u ? mine1 : mine0);
+              const uint32_t tS = tbase + L::T_S + u * 128 + h * 64;
+              if (x >= 0 && x < mine) {
+                if (!(ok = waitw(p_full + 2 * u + h, (odd >> u) & 1))) break;
+                odd ^= static_cast<uint32_t>(h) << u;
                 tc_fence_after();
-                const uint64_t v = dV + (tile & 1) * 2048;
-                const uint32_t tP = tbase + L::T_S + u * 128, tO = tbase + L::T_O + u * 128;
+                const uint64_t v = dV + (now & 1) * 2048 + h * 1024;
+                const uint32_t tO = tbase + L::T_O + u * 128;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)           // O_u += P_u V
-                  mma_f16_ta_elect(tO, tP + kk * 8, v + (kk >> 2) * 1024 + (kk & 3) * 2, idesc, (t == 0 && kk == 0) ? 0u : 1u);
-                if (t + 1 == mine) mma_commit_elect(o_full + u);
+                for (int kk = 0; kk < 4; ++kk)           // O_u += P_u V
+                  mma_f16_ta_elect(tO, tS + kk * 8, v + kk * 2, idesc_pv, (x == 0 && kk == 0) ? 0u : 1u);
+                mma_commit_elect(pv_done + 2 * u + h);
               }
-              if (t + 1 < mine) {
-                const int nx = t < 0 ? tile : tile + 1;
-                ok = k_in || waitw(k_full + (nx & 1), (nx >> 1) & 1);
-                if (!ok) break;
-                k_in = true;
+              if (x + 2 < mine) {
                 tc_fence_after();
-                qk(u, nx);
+                const uint64_t q = dQ + u * 2048, k = dK + (nx & 1) * 2048 + h * 512;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)           // S_u = Q_u K^T
+                  mma_f16_elect(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+                mma_commit_elect(s_full + 2 * u + h);
               }
             }
             if (!ok) break;
-            if (t + 1 < len) mma_commit_elect(k_empty + ((t < 0 ? tile : tile + 1) & 1));
-            if (t + 2 == len) mma_commit_elect(q_empty);
-            if (t >= 0) {
-              mma_commit_elect(v_empty + (tile & 1));
-              ++tile;
+            if (h == 1) {
+              if (x + 2 < 2 * len) mma_commit_elect(k_empty + (nx & 1));
+              if (x + 3 == 2 * len) mma_commit_elect(q_empty);
+              if (x > 0) mma_commit_elect(v_empty + (now & 1));
             }
           }
           if (!ok) break;
+          tile += len;
         }
         mma_commit_elect(mma_final);
         mbar_wait(mma_final, 0);
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tbase + L::T_S + unit * 128 + lane_addr, tO = tbase + L::T_O + unit * 128 + lane_addr;
     bool ok = true;
-    int tile = 0, n = 0, n_o = 0;                        // tiles; of this unit; segments with any
+    int tile = 0, n = 0;                                 // tiles; half tiles of this unit
     for (int seg = 0;; ++seg) {
       if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1)) break;
       const PromptSeg& g = seg_at(seg);
@@ -605,97 +605,85 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
       const int lim_min = g.ctx - g.n + t0 - g.j0 * 128; // the last key that every row of the unit sees, from the segment's first
       float m_ref = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int t = 0; t < mine; ++t, ++n) {
-        if (!waitw(s_full + unit, n & 1)) { ok = false; break; }
-        tc_fence_after();
-        const int gone = missing[(tile + t) & 7];
-        if (t * 128 + 127 > lim_min || gone != 0) {      // keys that not every row sees: masked in place
-          const int last = lim_min + row_map[row].x - t * 128;
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
+      for (int x = 0; x < 2 * mine; ++x, ++n) {           // half tiles
+        const int h = x & 1;
+        const uint32_t tSh = tS + h * 64;
+        if (!waitw(s_full + 2 * unit + h, (n >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const bool gone = missing[(tile + (x >> 1)) & 7] >> h & 1;
+        if (x * 64 + 63 > lim_min || gone) {             // keys that not every row sees: masked in place
+          const int last = gone ? -1 : lim_min + row_map[row].x - x * 64;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
             uint32_t y[16];
-            tmem_ld16(tS + c, y);
+            tmem_ld16(tSh + c, y);
             tmem_wait_ld();
-            const int end = (gone & (c < 64 ? 1 : 2)) ? -1 : last - c;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] = k <= end ? y[k] : 0xFF800000u;
-            tmem_st16(tS + c, y);
+            for (int k = 0; k < 16; ++k) y[k] = c + k <= last ? y[k] : 0xFF800000u;
+            tmem_st16(tSh + c, y);
           }
           tmem_wait_st();
         }
-        // the scores are read twice, piece by piece: the maximum, then the weights, which take
-        // the place of scores already read (all 128 in registers would cost the code of 128, which,
-        // with the other roles', passes the instruction cache)
-        float m2[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {
-          uint32_t y[64];
-          tmem_ld32(tS + c, y);
-          tmem_ld32(tS + c + 32, y + 32);
-          tmem_wait_ld();
+        uint32_t y[64];
+        tmem_ld32(tSh, y);
+        tmem_ld32(tSh + 32, y + 32);
+        tmem_wait_ld();
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            m2[0] = fmax3(m2[0], __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-            m2[1] = fmax3(m2[1], __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
-          }
+        for (int k = 0; k < 64; k += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], __uint_as_float(y[k + 2 * i]), __uint_as_float(y[k + 2 * i + 1]));
         }
-        const float mt = fmaxf(m2[0], m2[1]) * C;
+        const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * C;
         // a row's first keys, or a rise past the limit: the reference follows
         if (__any_sync(0xffffffffu, mt > m_ref + kRiseLimit)) {
           const float m_new = fmaxf(m_ref, mt);
-          if (t > 0) {
+          if (x > 0) {
             const float al = m_new == -INFINITY ? 1.f : ex2_approx(m_ref - m_new);
             const float2 A = make_float2(al, al);
             l2[0] = __fmul2_rn(l2[0], A);
             l2[1] = __fmul2_rn(l2[1], A);
+            if (!waitw(pv_done + 2 * unit + (h ^ 1), ((n - 1) >> 1) & 1)) { ok = false; break; }   // the last half's is in O
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
+            for (int c = 0; c < 128; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; k += 2) {
+              for (int k = 0; k < 16; k += 2) {
                 const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), A);
                 o[k] = __float_as_uint(v.x);
                 o[k + 1] = __float_as_uint(v.y);
               }
-              tmem_st32(tO + c, o);
+              tmem_st16(tO + c, o);
             }
           }
           m_ref = m_new;
         }
         const float bias = kPShift - (m_ref == -INFINITY ? 0.f : m_ref);
         const float2 C2 = make_float2(C, C), B2 = make_float2(bias, bias);
-        uint32_t z[32];
-        tmem_ld32(tS, z);
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t y[32], p[16];
-          tmem_wait_ld();
+        uint32_t p[4][8];                                // P takes the place of the scores' first columns
 #pragma unroll
-          for (int k = 0; k < 32; ++k) y[k] = z[k];
-          if (c < 96) tmem_ld32(tS + c + 32, z);         // the next ones under these
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), C2, B2);
-            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
-            p[k >> 1] = pack_half2(e.x, e.y);
-          }
-          tmem_st16(tS + c / 2, p);
+        for (int k = 0; k < 64; k += 2) {
+          float2 e = __ffma2_rn(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), C2, B2);
+          e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+          l2[(k >> 1) & 1] = __fadd2_rn(l2[(k >> 1) & 1], e);
+          p[k >> 4][(k >> 1) & 7] = pack_half2(e.x, e.y);
+          if ((k & 15) == 14) tmem_st8(tSh + (k >> 4) * 8, p[k >> 4]);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + unit);
+        if (lane == 0) mbar_arrive(p_full + 2 * unit + h);
       }
       if (!ok) break;
       tile += g.len;
       // ---- O of the segment ----
       const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
       if (mine > 0) {
-        if (!waitw(o_full + unit, n_o & 1)) { ok = false; break; }
-        ++n_o;
+        if (!waitw(pv_done + 2 * unit + 1, ((n - 1) >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
       }
       // (thread's place read afresh: addresses computed from it before the tiles would stay in registers)

@@ -15,12 +15,12 @@
 // The key tiles of all items form one line, cut into equal ranges, one a CTA (kv4_range), whatever
 // the lengths and however few the rows; an item that crosses CTAs leaves partials.
 //
-// Roles (512 threads): warp 0 issues Q K^T, warp 1 P V, warps 2-3 bring in Q, warps 4-7 decode K and
-// V pages from global memory (prefetched into registers a tile ahead) into the tensor cores'
-// 128-byte-swizzled layout, warps 8-11 and 12-15 are the units' softmax.
-// TMEM (512 columns): one S that the units use in turn, P_0, P_1, O_0, O_1. S is free as soon as its
-// softmax has it in registers, so the next scores are computed under the exponentials (with a
-// buffer for each unit and P in its place they would have to wait for the product with P).
+// Roles (512 threads): warp 0 issues the products, warp 1 hands out the work and loads Q (TMA), warps
+// 4-7 decode K and V pages into the tensor cores' 128-byte-swizzled layout, warps 8-11 and 12-15 are the
+// units' softmax.
+// TMEM (512 columns): S_0, S_1 (two half tiles of 64 keys each; P of a half over its first 32 columns), O_0, O_1. The
+// scores of a half are issued as soon as the product with the P in its place is, so that a unit always has
+// one half's scores waiting while its softmax works on the other's.
 #pragma once
 #include "kv4_split.cuh"
 
@@ -44,18 +44,20 @@ __device__ __forceinline__ int64_t floor_sum128(int64_t n, int64_t a, int64_t b)
     a = t;
   }
 }
-// A sequence's items per KV head: T2 tokens each, and the key tiles (128 keys) each of them sees.
+// A sequence's items per KV head: T2 tokens each, the key tiles (128 keys) each of them sees, and the units of
+// work they count: its tiles, after one for the item itself (its Q, its O, filling the pipeline).
 struct PromptSeq {
   Kv4Seq q;
   int T2;
   __device__ __forceinline__ int items() const { return (q.n + T2 - 1) / T2; }
   __device__ __forceinline__ int tiles_to(int tok) const { return (q.ctx - q.n + tok + 127) >> 7; }  // seen by tokens < tok
   __device__ __forceinline__ int tiles(int i) const { return tiles_to(min(q.n, (i + 1) * T2)); }
-  __device__ __forceinline__ int64_t before(int i) const {          // tiles of the items before item i
+  __device__ __forceinline__ int units(int i) const { return tiles(i) + 1; }
+  __device__ __forceinline__ int64_t before(int i) const {          // units of the items before item i
     const int last = items();
     const int64_t k = i < last ? i : last - 1;
     const int64_t s = k > 0 ? floor_sum128(k, T2, static_cast<int64_t>(q.ctx - q.n) + T2 + 127) : 0;
-    return i < last ? s : s + tiles(last - 1);
+    return i + (i < last ? s : s + tiles(last - 1));
   }
 };
 
@@ -117,18 +119,21 @@ struct PromptWalk {
     j = static_cast<int>(at - sq.before(lo));
   }
   __device__ __forceinline__ bool next(const Kv4AttnArgs& a, PromptSeg& g) {
+    if (left == 1 && j == 0) left = 0;                   // an item's first unit alone: no tile, nothing to do
     if (left <= 0) return false;
-    const int nt = sq.tiles(i), j1 = min(nt, j + left), TU = sq.T2 / 2;
+    // j counts units: tiles j - 1 on, from 0
+    const int nt = sq.tiles(i), u1 = min(nt + 1, j + left), TU = sq.T2 / 2;
+    const int j0 = max(0, j - 1), j1 = u1 - 1;
     g.s = s; g.h = h; g.q0 = sq.q.q0; g.n = sq.q.n; g.ctx = sq.q.ctx;
     g.tok = i * sq.T2;
-    g.j0 = j; g.len = j1 - j;
+    g.j0 = j0; g.len = j1 - j0;
     const int nt0 = sq.tiles_to(min(sq.q.n, g.tok + TU));
     const int nt1 = g.tok + TU < sq.q.n ? nt : 0;
-    g.mine0 = max(0, min(j1, nt0) - j);
-    g.mine1 = max(0, min(j1, nt1) - j);
-    g.whole = j == 0 && j1 == nt;
+    g.mine0 = max(0, min(j1, nt0) - j0);
+    g.mine1 = max(0, min(j1, nt1) - j0);
+    g.whole = j0 == 0 && j1 == nt;
     g.first = j == 0;
-    left -= j1 - j;
+    left -= u1 - j;
     j = 0;
     if (left > 0 && ++i == sq.items()) {
       i = 0;
@@ -160,14 +165,9 @@ __device__ __forceinline__ int prefetch_id(const int32_t* p) {
 __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// 16-byte asynchronous copy, or zeros.
-__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool copy) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0)
-               : "memory");
-}
-
 template <typename T>
-__global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
+__global__ void __launch_bounds__(512, 1)
+kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
   using L = PromptLayout;
   constexpr bool kConvertQ = std::is_same<T, __nv_bfloat16>::value;
   // at a fixed, 1024-byte aligned address (there is no other shared memory): every address in it is a
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
   }
   if (threadIdx.x < 128) row_map[threadIdx.x] = make_uchar2(threadIdx.x / group, threadIdx.x % group);
   if (threadIdx.x == 0) {
-    mbar_init(q_raw, 2);
-    mbar_init(q_full, kConvertQ ? 8 : 2);
+    mbar_init(q_raw, 1);
+    mbar_init(q_full, kConvertQ ? 8 : 1);
     mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 2);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     mbar_init(mma_final, 1);
     for (int i = 0; i < L::NSEG; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 1 + 2 + 4 + 8);           // products, Q, decoding, softmax
+      mbar_init(seg_empty + i, 1 + 1 + 4 + 8);           // products, Q, decoding, softmax
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -336,12 +336,12 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         __syncwarp();
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // (its registers serve the others of the warpgroup)
-    } else {
-      // ================================ segments and Q ================================
-      // One thread hands out the segments, two ahead of the one whose Q is brought in (its slot's last
-      // user is done by then: see the wait for q_empty).
+    } else if (warp == 1 && lane == 0) {
+      // ======================= segments and Q (one thread) =======================
+      // Hands out the segments, two ahead of the one whose Q is brought in, and loads Q: per unit two boxes of
+      // 64 channels x the group's heads x TU tokens, rows being (token, head). (Tokens of another sequence
+      // behind this one's are loaded too and nobody's rows; behind the last token: zeros.)
+      prefetch_tmap(&tm_q);
       PromptWalk* const walk = reinterpret_cast<PromptWalk*>(sm + L::OFF_WALK);   // (no registers for it)
       int handed = 0;
       auto hand_out = [&]() {
@@ -350,47 +350,29 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
         mbar_arrive(seg_full + handed % L::NSEG);
         ++handed;
       };
-      if (warp == 3 && lane == 0) {
-        walk->start(a, rng);
-        hand_out();
-        hand_out();
-      }
-      __syncwarp();
-      // Copied as it is, half a warp a row, 16 bytes a thread; rows without a token are zero. The
-      // eights of channels are stored in K's order (see the decoding). (bf16: the softmax warps make
-      // it fp16 in place.)
-      const int hw = lane >> 4, ch = lane & 15;
-      const int pos = ((ch & 8) << 11) | (((ch & 7) ^ ((ch & 8) >> 1)) << 4);
-      for (int seg = 0;; ++seg) {
-        if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1)) break;
+      walk->start(a, rng);
+      hand_out();
+      hand_out();
+      int seg = 0;
+      for (;; ++seg) {
         const PromptSeg& g = seg_at(seg);
         if (g.s < 0) break;
-        const int left = g.n - g.tok;                    // tokens from the item's first on
-        const T* q = static_cast<const T*>(a.q) + (g.q0 + g.tok) * a.q_stride + g.h * group * kKv4D + ch * 8;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
         // the last segment's products have read Q
-        if (seg > 0 && !waitw(q_empty, (seg - 1) & 1)) break;
-        if (warp == 3 && lane == 0 &&
-            (handed < L::NSEG || wait1(seg_empty + handed % L::NSEG, (handed / L::NSEG - 1) & 1)))
-          hand_out();
-        __syncwarp();
-#pragma unroll 2
-        for (int r = (warp - 2) * 2 + hw; r < 256; r += 4) {
-          const int ru = r & 127;
-          const uchar2 at = row_map[ru];
-          const int tok = (r >> 7) * TU + at.x;
-          const bool real = ru < TU * group && tok < left;
-          cp_async16_or_zero(sm + L::OFF_Q + (r >> 7) * 32768 + ru * 128 + (pos ^ ((ru & 7) << 4)),
-                               real ? q + tok * a.q_stride + at.y * kKv4D : q, real);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kConvertQ ? q_raw : q_full);
+        if (seg > 0 && !wait1(q_empty, (seg - 1) & 1)) break;
+        uint64_t* bar = kConvertQ ? q_raw : q_full;
+        mbar_arrive_expect_tx(bar, 4 * 128 * TU * group);
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b)
+          tma_load_3d(sm + L::OFF_Q + b * 16384, &tm_q, bar, (b & 1) * 64, g.h * group, g.q0 + g.tok + (b >> 1) * TU);
+        mbar_arrive(seg_empty + seg % L::NSEG);
+        // the slot's last user: the segment two before this one
+        if (handed >= L::NSEG && !wait1(seg_empty + handed % L::NSEG, (handed / L::NSEG - 1) & 1)) { ++seg; break; }
+        hand_out();
       }
+      // never leave a copy in flight into this CTA's shared memory
+      if (seg > 0) mbar_wait(kConvertQ ? q_raw : q_full, (seg - 1) & 1);
     }
+    __syncwarp();
   } else if (warp < 8) {
     // ============================ K and V decoding ============================
     // Warps 4 and 5 decode K, warps 6 and 7 V, tile by tile. Codes and scales come a tile ahead, by
@@ -437,10 +419,10 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
     bool more = false, after = false;
     if (warp < 6) {
       // K: a thread has half the channels of rows kr and kr + 32 of a page: a row's eight words of eight channels
-      // become eight 16-byte chunks. Of the upper half, chunks c and c ^ 4 trade places, so that the eight
-      // threads of four rows write to eight different banks of 16 bytes; Q has the same order.
+      // become eight 16-byte chunks, four at a time. The threads of the upper half begin with the last four, so
+      // that the eight threads of four rows write to eight different banks of 16 bytes.
       const int kr = tid >> 1, kh = tid & 1;
-      const uint32_t kpos = static_cast<uint32_t>(((kh * 4) ^ (kr & 7)) << 4);   // a word's chunk in its row, but for the word
+      const uint32_t kpos = static_cast<uint32_t>((kr & 7) << 4);   // a word's chunk in its row, but for the word
       unsigned char* codes = sm + L::OFF_CODES + tid * 16;          // [page][row][2][64] 16 bytes
       unsigned char* scales = sm + L::OFF_CODES + 8192 + tid * 4;   // [page][row][64] 4 bytes
       for (int tile = -2;; ++tile) {
@@ -458,12 +440,13 @@ __global__ void __launch_bounds__(512, 1) kv4_prompt_kernel(Kv4AttnArgs a) {
           const int pg = it >> 2;
           if (more) {
             if ((it & 3) == 0) cp_async_wait<1>();
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + (it >> 1) * 256 + (it & 1) * 2);
+            const int o = (it & 1) ^ kh;                 // which four of the row's words
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + (it >> 1) * 256 + o * 2);
             const __half2 s2 = e4m3x2_to_half2(valid(pg ? now.id1 : now.id0) ? sc : 0u);
-            const uint4 c = *reinterpret_cast<const uint4*>(codes + it * 1024);
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + (it >> 1) * 2048 + o * 1024);
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
             unsigned char* dst = row + (it >> 1) * 4096;
-            const uint32_t pos = kpos ^ ((it & 1) << 6);
+            const uint32_t pos = kpos ^ static_cast<uint32_t>(o << 6);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __half2 f = e < 2 ? __low2half2(s2) : __high2half2(s2);
@@ -774,7 +757,10 @@ __global__ void __launch_bounds__(256) kv4_prompt_merge_kernel(Kv4AttnArgs a) {
   }
   const int64_t first = at - (r - sq.before(i0));        // the item's first unit
   if (first == at || first / per != cta - 1) return;     // not cut here, or not here first
-  const int c1 = static_cast<int>((first + sq.tiles(i0) - 1) / per);
+  const int c1 = static_cast<int>((first + sq.units(i0) - 1) / per);
+  // (a first unit alone at the end of a CTA's range has left no partial)
+  const int c0 = at - first == 1 ? cta : cta - 1;
+  if (c0 == c1) return;                                  // written by the prompt kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, TU = sq.T2 / 2;
   auto part = [&](int c) {
     return a.prompt_part + static_cast<int64_t>(2 * c + (c == cta - 1 ? 1 : 0)) * kPromptPartFloats;
@@ -784,11 +770,11 @@ __global__ void __launch_bounds__(256) kv4_prompt_merge_kernel(Kv4AttnArgs a) {
     const int tok = i0 * sq.T2 + (row >> 7) * TU + ru / group;
     if (ru >= TU * group || tok >= sq.q.n) continue;
     float M = -INFINITY;
-    for (int c = cta - 1; c <= c1; ++c) M = fmaxf(M, part(c)[256 * kKv4D + row]);
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, part(c)[256 * kKv4D + row]);
     const float mu = M == -INFINITY ? 0.f : M;
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = cta - 1; c <= c1; ++c) {
+    for (int c = c0; c <= c1; ++c) {
       const float* p = part(c);
       const float w = ex2_approx(p[256 * kKv4D + row] - mu);
       const float4 v = *reinterpret_cast<const float4*>(p + row * kKv4D + lane * 4);

@@ -881,7 +881,7 @@ Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
   s.split_ctas = ctas(heads * ((p->max_context - 1) / 64 + 1), 4);
   const int64_t tokens = 2 * (128 / group), items = (p->max_q - 1) / tokens + 1;
   const int64_t tiles = (p->max_context - 1) / 128 + 1;
-  s.prompt_ctas = ctas(heads > sms || items > sms || tiles > sms ? sms * 2 : heads * items * tiles, 2);
+  s.prompt_ctas = ctas(heads > sms || items > sms || tiles > sms ? sms * 2 : heads * items * (tiles + 1), 2);
   const size_t plan = (8 * (static_cast<size_t>(p->num_seqs) + 1) + 15) / 16 * 16;
   s.part_off = plan;
   s.prompt_plan_off = s.split ? s.part_off + static_cast<size_t>(s.split_ctas) * 2 * kKv4PartFloats * 4 : 0;
@@ -922,9 +922,16 @@ qk4v8_status launch_kv4_split(const Kv4AttnArgs& a, int ctas, cudaStream_t strea
 template <typename T>
 qk4v8_status launch_kv4_prompt(const Kv4AttnArgs& a, int ctas, cudaStream_t stream) {
   using L = PromptLayout;
+  CUtensorMap tq;                               // Q: boxes of 64 channels x a group's heads x a unit's tokens
+  const uint32_t group = static_cast<uint32_t>(a.Hq / a.c.Hkv);
+  const uint64_t dims[3] = {kKv4D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.total_q)};
+  const uint64_t strides[2] = {kKv4D * 2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint32_t box[3] = {64, group, 128 / group};
+  const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (!make_map(&tq, dt, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return QK4V8_ERR_CUDA;
   static PerDeviceOnce opt_in;
   if (!opt_in.run(current_device(), [] { return set_smem(kv4_prompt_kernel<T>, L::SMEM_ALLOC); })) return QK4V8_ERR_CUDA;
-  kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_ALLOC, stream>>>(a);
+  kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_ALLOC, stream>>>(tq, a);
   if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
   if (ctas > 1) kv4_prompt_merge_kernel<T><<<dim3(ctas - 1, 8), 256, 0, stream>>>(a);
   return launch_status();

@@ -71,15 +71,15 @@ struct PromptSeg {
 };                                                       // (s = -1: no more)
 struct PromptLayout {
   static constexpr int OFF_Q = 0;                        // [unit] 2 x 16 KB (64 channels each)
-  static constexpr int OFF_K = 65536;                    // [stage] 2 x 16 KB (64 channels each)
-  static constexpr int OFF_V = OFF_K + 65536;            // [stage] 2 x 16 KB (64 tokens each)
+  static constexpr int OFF_K = 65536;                    // [4] pages, 2 x 8 KB (64 channels each)
+  static constexpr int OFF_V = OFF_K + 65536;            // [4] pages, 16 KB
   static constexpr int OFF_CODES = OFF_V + 65536;        // the next tile's codes and scales, K's and V's
   static constexpr int OFF_MAP = OFF_CODES + 2 * 9216;   // [128] a row's token and head within the unit
-  static constexpr int OFF_FLAG = OFF_MAP + 256;        // [8] pages missing, by tile
-  static constexpr int OFF_RANGE = OFF_FLAG + 32;
+  static constexpr int OFF_FLAG = OFF_MAP + 256;        // [16] whether the page is missing
+  static constexpr int OFF_RANGE = OFF_FLAG + 64;
   static constexpr int OFF_BAR = OFF_RANGE + (sizeof(Kv4Range) + 7) / 8 * 8;
   static constexpr int NSEG = 4;                         // segments handed out ahead
-  static constexpr int N_BARS = 24 + 2 * NSEG;
+  static constexpr int N_BARS = 32 + 2 * NSEG;
   static constexpr int OFF_SEG = (OFF_BAR + N_BARS * 8 + 16 + 15) / 16 * 16;
   static constexpr int OFF_WALK = OFF_SEG + NSEG * 64;
   static constexpr int SMEM_BYTES = OFF_WALK + 64;
@@ -177,18 +177,18 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::OFF_BAR);
   uint64_t* q_full = bars;                               // Q of the segment is in place
   uint64_t* q_empty = bars + 1;                          // its last QK^T is done
-  uint64_t* k_full = bars + 2;                           // [2]
-  uint64_t* k_empty = bars + 4;                          // [2]
-  uint64_t* v_full = bars + 6;                           // [2]
-  uint64_t* v_empty = bars + 8;                          // [2]
-  uint64_t* s_full = bars + 10;                          // [unit][half tile] its scores are ready
-  uint64_t* p_full = bars + 14;                          // [unit][half tile] P written over its scores
-  uint64_t* pv_done = bars + 18;                         // [unit][half tile] its product with V is done
+  uint64_t* k_full = bars + 2;                           // [4] a page of K, of V: decoded, used
+  uint64_t* k_empty = bars + 6;
+  uint64_t* v_full = bars + 10;
+  uint64_t* v_empty = bars + 14;
+  uint64_t* s_full = bars + 18;                          // [unit][half tile] its scores are ready
+  uint64_t* p_full = bars + 22;                          // [unit][half tile] P written over its scores
+  uint64_t* pv_done = bars + 26;                         // [unit][half tile] its product with V is done
   // (Barriers for each half: a softmax may be two halves ahead of the products, and nobody may wait two
   // phases behind. It is never further ahead: a half's scores are issued after its last product.)
-  uint64_t* mma_final = bars + 22;
-  uint64_t* q_raw = bars + 23;                           // Q has been copied in, to be converted
-  uint64_t* seg_full = bars + 24;                        // [NSEG]
+  uint64_t* mma_final = bars + 30;
+  uint64_t* q_raw = bars + 31;                           // Q has been copied in, to be converted
+  uint64_t* seg_full = bars + 32;                        // [NSEG]
   uint64_t* seg_empty = seg_full + L::NSEG;              // [NSEG]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -207,22 +207,19 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     mbar_init(q_raw, 1);
     mbar_init(q_full, kConvertQ ? 8 : 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(k_full + i, 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(k_full + i, 4);
       mbar_init(k_empty + i, 1);
       mbar_init(v_full + i, 2);
       mbar_init(v_empty + i, 1);
-      mbar_init(s_full + 2 * i, 1);
-      mbar_init(s_full + 2 * i + 1, 1);
-      mbar_init(p_full + 2 * i, 4);
-      mbar_init(p_full + 2 * i + 1, 4);
-      mbar_init(pv_done + 2 * i, 1);
-      mbar_init(pv_done + 2 * i + 1, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(pv_done + i, 1);
     }
     mbar_init(mma_final, 1);
     for (int i = 0; i < L::NSEG; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 1 + 1 + 4 + 8);           // products, Q, decoding, softmax
+      mbar_init(seg_empty + i, 1 + 1 + 6 + 8);           // products, Q, decoding, softmax
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -268,7 +265,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     return true;
   };
 
-  if (warp < 4) {
+  if (warp < 2) {
     if (warp == 0) {
       // ======================= products =======================
       {
@@ -294,9 +291,9 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
           // half x with V, and the scores of half x + 2 in its place.
 #pragma unroll 1
           for (int x = -2; x < 2 * len && ok; ++x) {
-            const int h = x & 1, now = tile + (x >> 1), nx = now + 1;     // tiles of halves x and x + 2
-            if (x + 2 < 2 * len && h == 0 && !(ok = waitw(k_full + (nx & 1), (nx >> 1) & 1))) break;
-            if (x >= 0 && h == 0 && !(ok = waitw(v_full + (now & 1), (now >> 1) & 1))) break;
+            const int h = x & 1, now = 2 * tile + x, nx = now + 2;        // pages of halves x and x + 2
+            if (x + 2 < 2 * len && !(ok = waitw(k_full + (nx & 3), (nx >> 2) & 1))) break;
+            if (x >= 0 && !(ok = waitw(v_full + (now & 3), (now >> 2) & 1))) break;
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
               const int mine = 2 * (u ? mine1 : mine0);
@@ -305,7 +302,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
                 if (!(ok = waitw(p_full + 2 * u + h, (odd >> u) & 1))) break;
                 odd ^= static_cast<uint32_t>(h) << u;
                 tc_fence_after();
-                const uint64_t v = dV + (now & 1) * 2048 + h * 1024;
+                const uint64_t v = dV + (now & 3) * 1024;
                 const uint32_t tO = tbase + L::T_O + u * 128;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)           // O_u += P_u V
@@ -314,19 +311,17 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
               }
               if (x + 2 < mine) {
                 tc_fence_after();
-                const uint64_t q = dQ + u * 2048, k = dK + (nx & 1) * 2048 + h * 512;
+                const uint64_t q = dQ + u * 2048, k = dK + (nx & 3) * 1024;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)           // S_u = Q_u K^T
-                  mma_f16_elect(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 1024 + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+                  mma_f16_elect(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 512 + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
                 mma_commit_elect(s_full + 2 * u + h);
               }
             }
             if (!ok) break;
-            if (h == 1) {
-              if (x + 2 < 2 * len) mma_commit_elect(k_empty + (nx & 1));
-              if (x + 3 == 2 * len) mma_commit_elect(q_empty);
-              if (x > 0) mma_commit_elect(v_empty + (now & 1));
-            }
+            if (x + 2 < 2 * len) mma_commit_elect(k_empty + (nx & 3));
+            if (x + 3 == 2 * len) mma_commit_elect(q_empty);
+            if (x >= 0) mma_commit_elect(v_empty + (now & 3));
           }
           if (!ok) break;
           tile += len;
@@ -375,78 +370,81 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     __syncwarp();
   } else if (warp < 8) {
     // ============================ K and V decoding ============================
-    // Warps 4 and 5 decode K, warps 6 and 7 V, tile by tile. Codes and scales come a tile ahead, by
-    // asynchronous copies that each thread makes for itself: a page's part that it has decoded it replaces
-    // by the same one of the next tile, whose page ids it has read a tile before that. A page that
-    // does not exist leaves what was there (codes are always finite) and counts with scale 0.
-    // (Loops over the pages stay loops: with all roles unrolled the code of a tile passes the
-    // instruction cache, and a decoded word cost five times its instructions.)
-    const int tid = threadIdx.x & 63;
-    struct Place {                                       // of a tile: its pages (-1: none), KV head, slots in the context
-      int id0, id1, h, left;
+    // Warps 2 to 5 decode K, warps 6 and 7 V, page by page into rings of four. Codes and scales come
+    // two pages ahead, by asynchronous copies that each thread makes for itself; the page's id has been
+    // read a page before that. A page that does not exist leaves what was there (codes are always
+    // finite) and counts with scale 0. (Loops stay loops: with all roles unrolled the code of a tile
+    // passes the instruction cache, and a decoded word cost five times its instructions.)
+    const bool is_v = warp >= 6;
+    struct Page {
+      int id, h, left;                                   // -1: none; KV head; slots in the context
     };
-    int seg = -1, tiles = 0, seg_h = 0, left = 0;
+    int seg = -1, pages = 0, seg_h = 0, left = 0;
     const int32_t* ids = nullptr;
-    auto next_tile = [&](int& id0, int& id1) -> bool {
-      if (--tiles < 0) {
+    bool end = false;
+    auto next_page = [&]() -> Page {
+      if (end) return Page{-1, 0, 0};
+      if (--pages < 0) {
         if (seg >= 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
         }
         ++seg;
         if (!waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1) || seg_at(seg).s < 0) {
-          tiles = 0;
-          return false;
+          end = true;
+          return Page{-1, 0, 0};
         }
         const PromptSeg& g = seg_at(seg);
-        tiles = g.len - 1;
+        pages = 2 * g.len - 1;
         seg_h = g.h;
         left = g.ctx - g.j0 * 128;
         ids = a.table + static_cast<int64_t>(g.s) * a.max_pages + 2 * g.j0;
       }
-      id0 = prefetch_id(ids);
-      id1 = -1;
-      if (left > 64) id1 = prefetch_id(ids + 1);
-      left -= 128;
-      ids += 2;
-      return true;
+      Page p = {-1, seg_h, left};
+      if (left > 0) p.id = prefetch_id(ids);
+      left -= 64;
+      ++ids;
+      return p;
     };
     auto valid = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.num_pages); };
-    // tiles now (being decoded), next (being loaded), third (its ids being read); the pipeline fills
-    // in two rounds without a tile, -2 and -1
-    Place now = {-1, -1, 0, 0}, next = now;
-    int third0 = -1, third1 = -1;
-    bool more = false, after = false;
-    if (warp < 6) {
-      // K: a thread has half the channels of rows kr and kr + 32 of a page: a row's eight words of eight channels
-      // become eight 16-byte chunks, four at a time. The threads of the upper half begin with the last four, so
-      // that the eight threads of four rows write to eight different banks of 16 bytes.
-      const int kr = tid >> 1, kh = tid & 1;
-      const uint32_t kpos = static_cast<uint32_t>((kr & 7) << 4);   // a word's chunk in its row, but for the word
-      unsigned char* codes = sm + L::OFF_CODES + tid * 16;          // [page][row][2][64] 16 bytes
-      unsigned char* scales = sm + L::OFF_CODES + 8192 + tid * 4;   // [page][row][64] 4 bytes
-      for (int tile = -2;; ++tile) {
-        const int stg = tile & 1;
-        const bool far = (after || tile == -2) && next_tile(third0, third1);
-        if (tile >= 2 && !waitw(k_empty + stg, ((tile >> 1) - 1) & 1)) break;
-        if (tid == 0 && more) {
-          const int gone = (valid(now.id0) ? 0 : 1) | (now.left <= 64 || valid(now.id1) ? 0 : 2);
-          missing[tile & 7] = gone;
-          if (gone) flag_error(kStatusBounds);
-        }
-        unsigned char* row = sm + L::OFF_K + stg * 32768 + kh * 16384 + kr * 128;
+    // pages p0 (being decoded), p1, p2 (to be loaded), and the one whose id is being read; count: pages that
+    // there are in all, known at the end. Three rounds without a page fill the pipeline.
+    Page p0 = {-1, 0, 0}, p1 = p0, p2 = p0;
+    int have = 0;                                        // pages handed out so far
+    const int tid = is_v ? (threadIdx.x & 63) : threadIdx.x - 64;
+    // K: a thread has half the channels of a row: eight words of eight channels become eight 16-byte
+    // chunks, four at a time. The threads of the upper half begin with the last four, so that the eight threads
+    // of four rows write to eight different banks of 16 bytes.
+    // V: a thread has eight tokens of 16 channels: four token pairs of a channel are a chunk.
+    const int kr = tid >> 1, kh = tid & 1, vt = tid & 7, vb = tid >> 3;
+    unsigned char* codes = sm + L::OFF_CODES + (is_v ? 9216 : 0) + tid * 16;   // K: [slot][2][128], V: [slot][4][64]
+    unsigned char* scales = sm + L::OFF_CODES + 8192 + (is_v ? 9216 + tid * 8 : tid * 4);
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
+    for (int g = -3;; ++g) {
+      const int stg = g & 3, slot = g & 1;
+      const Page p3 = next_page();
+      if (!end) ++have;
+      if (g >= 0) {
+        if (g >= have) break;
+        if (g >= 4 && !waitw(empty + stg, ((g >> 2) - 1) & 1)) break;
+        cp_async_wait<1>();
+        const bool there = valid(p0.id);
+        if (!is_v) {
+          if (tid == 0) {
+            const int gone = !there && p0.left > 0;
+            missing[g & 15] = gone;
+            if (gone) flag_error(kStatusBounds);
+          }
+          unsigned char* row = sm + L::OFF_K + stg * 16384 + kh * 8192 + kr * 128;
 #pragma unroll 1
-        for (int it = 0; it < 8; ++it) {                 // page it / 4, row kr + 32 (it / 2 % 2), four words
-          const int pg = it >> 2;
-          if (more) {
-            if ((it & 3) == 0) cp_async_wait<1>();
-            const int o = (it & 1) ^ kh;                 // which four of the row's words
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + (it >> 1) * 256 + o * 2);
-            const __half2 s2 = e4m3x2_to_half2(valid(pg ? now.id1 : now.id0) ? sc : 0u);
-            const uint4 c = *reinterpret_cast<const uint4*>(codes + (it >> 1) * 2048 + o * 1024);
+          for (int it = 0; it < 2; ++it) {
+            const int o = it ^ kh;                       // which four of the row's words
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + slot * 512 + o * 2);
+            const __half2 s2 = e4m3x2_to_half2(there ? sc : 0u);
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + slot * 4096 + o * 2048);
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
-            unsigned char* dst = row + (it >> 1) * 4096;
-            const uint32_t pos = kpos ^ static_cast<uint32_t>(o << 6);
+            const uint32_t pos = static_cast<uint32_t>(((kr & 7) << 4) ^ (o << 6));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const __half2 f = e < 2 ? __low2half2(s2) : __high2half2(s2);
@@ -454,96 +452,57 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
               e2m1x8_to_half2(w[e], d);
 #pragma unroll
               for (int x = 0; x < 4; ++x) d[x] = hmul2(d[x], f);
-              *reinterpret_cast<uint4*>(dst + (pos ^ (e << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
+              *reinterpret_cast<uint4*>(row + (pos ^ (e << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
             }
           }
-          if ((it & 3) == 3) {
-            const int id = pg ? next.id1 : next.id0;
-            if (after && valid(id)) {
-              const int64_t head = static_cast<int64_t>(id) * a.c.Hkv + next.h;
-              const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32;
-              const uint8_t* s = a.c.k_scales + head * 512 + kr * 8 + kh * 4;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                cp_async16(codes + pg * 4096 + i * 2048, k + i * 2048);
-                cp_async16(codes + pg * 4096 + i * 2048 + 1024, k + i * 2048 + 16);
-                cp_async4(scales + pg * 512 + i * 256, s + i * 256, true);
-              }
-            }
-            cp_async_commit();
+        } else {
+          uint2 sc = *reinterpret_cast<const uint2*>(scales + slot * 512);
+          const int in = there ? p0.left - vt * 8 : 0;   // of the thread's slots, those in the context
+          if (in < 8) {                                  // the others: value 0 (weight 0 x NaN is not 0)
+            const uint64_t keep = in <= 0 ? 0 : (1ull << (8 * in)) - 1;
+            sc.x &= static_cast<uint32_t>(keep);
+            sc.y &= static_cast<uint32_t>(keep >> 32);
           }
-        }
-        if (more) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(k_full + stg);
-        }
-        now = next;
-        next = Place{third0, third1, seg_h, left + 128};   // (the walk has not moved since)
-        more = after;
-        after = far;
-        if (!more && !after) break;
-      }
-    } else {
-      // V: a thread has eight tokens of 16 channels of each page: four token pairs of a channel are a chunk.
-      const int vt = tid & 7, vb = tid >> 3;
-      unsigned char* codes = sm + L::OFF_CODES + 9216 + tid * 16;          // [page][token pair][64] 16 bytes
-      unsigned char* scales = sm + L::OFF_CODES + 9216 + 8192 + tid * 8;   // [page][64] 8 bytes
-      for (int tile = -2;; ++tile) {
-        const int stg = tile & 1;
-        const bool far = (after || tile == -2) && next_tile(third0, third1);
-        if (tile >= 2 && !waitw(v_empty + stg, ((tile >> 1) - 1) & 1)) break;
-        unsigned char* row = sm + L::OFF_V + stg * 32768 + vb * 16 * 128;
+          const __half2 f[4] = {e4m3x2_to_half2(sc.x & 0xFFFFu), e4m3x2_to_half2(sc.x >> 16),
+                                e4m3x2_to_half2(sc.y & 0xFFFFu), e4m3x2_to_half2(sc.y >> 16)};
+          unsigned char* row = sm + L::OFF_V + stg * 16384 + vb * 16 * 128;
 #pragma unroll 1
-        for (int pg = 0; pg < 2; ++pg, row += 16384) {
-          if (more) {
-            cp_async_wait<1>();
-            uint2 sc = *reinterpret_cast<const uint2*>(scales + pg * 512);
-            const int in = valid(pg ? now.id1 : now.id0) ? now.left - pg * 64 - vt * 8 : 0;   // slots in the context
-            if (in < 8) {                                // the others: value 0 (weight 0 x NaN is not 0)
-              const uint64_t keep = in <= 0 ? 0 : (1ull << (8 * in)) - 1;
-              sc.x &= static_cast<uint32_t>(keep);
-              sc.y &= static_cast<uint32_t>(keep >> 32);
+          for (int e = 0; e < 4; ++e, row += 512) {
+            uint32_t d[4][4];                            // [token pair][channel 4 e + x]
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(codes + slot * 4096 + k * 1024 + e * 4), d[k]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) d[k][x] = hmul2(d[k][x], f[k]);
             }
-            const __half2 f[4] = {e4m3x2_to_half2(sc.x & 0xFFFFu), e4m3x2_to_half2(sc.x >> 16),
-                                  e4m3x2_to_half2(sc.y & 0xFFFFu), e4m3x2_to_half2(sc.y >> 16)};
-#pragma unroll 1
-            for (int e = 0; e < 4; ++e) {
-              uint32_t d[4][4];                          // [token pair][channel 4 e + x]
+            const uint32_t pos = static_cast<uint32_t>(vt ^ ((e & 1) * 4)) << 4;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(codes + pg * 4096 + k * 1024 + e * 4), d[k]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) d[k][x] = hmul2(d[k][x], f[k]);
-              }
-              unsigned char* dst = row + e * 512;
-              const uint32_t pos = static_cast<uint32_t>(vt ^ ((e & 1) * 4)) << 4;
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(dst + x * 128 + (pos ^ (x << 4))) = make_uint4(d[0][x], d[1][x], d[2][x], d[3][x]);
-            }
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(row + x * 128 + (pos ^ (x << 4))) = make_uint4(d[0][x], d[1][x], d[2][x], d[3][x]);
           }
-          const int id = pg ? next.id1 : next.id0;
-          if (after && valid(id)) {
-            const int64_t head = static_cast<int64_t>(id) * a.c.Hkv + next.h;
-            const uint8_t* v = a.c.v_pages + head * 4096 + vt * 512 + vb * 16;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) cp_async16(codes + pg * 4096 + k * 1024, v + k * 128);
-            cp_async8(scales + pg * 512, a.c.v_scales + head * 512 + vb * 64 + vt * 8);
-          }
-          cp_async_commit();
         }
-        if (more) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(v_full + stg);
-        }
-        now = next;
-        next = Place{third0, third1, seg_h, left + 128};   // (the walk has not moved since)
-        more = after;
-        after = far;
-        if (!more && !after) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + stg);
       }
+      if (valid(p2.id)) {                                // into the place of the page just decoded
+        const int64_t head = static_cast<int64_t>(p2.id) * a.c.Hkv + p2.h;
+        if (!is_v) {
+          const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32;
+          cp_async16(codes + slot * 4096, k);
+          cp_async16(codes + slot * 4096 + 2048, k + 16);
+          cp_async4(scales + slot * 512, a.c.k_scales + head * 512 + kr * 8 + kh * 4, true);
+        } else {
+          const uint8_t* v = a.c.v_pages + head * 4096 + vt * 512 + vb * 16;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) cp_async16(codes + slot * 4096 + k * 1024, v + k * 128);
+          cp_async8(scales + slot * 512, a.c.v_scales + head * 512 + vb * 64 + vt * 8);
+        }
+      }
+      cp_async_commit();
+      p0 = p1;
+      p1 = p2;
+      p2 = p3;
     }
   } else {
     // ================================ softmax ================================
@@ -594,7 +553,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         const uint32_t tSh = tS + h * 64;
         if (!waitw(s_full + 2 * unit + h, (n >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
-        const bool gone = missing[(tile + (x >> 1)) & 7] >> h & 1;
+        const bool gone = missing[(2 * tile + x) & 15] != 0;
         if (x * 64 + 63 > lim_min || gone) {             // keys that not every row sees: masked in place
           const int last = gone ? -1 : lim_min + row_map[row].x - x * 64;
 #pragma unroll 1

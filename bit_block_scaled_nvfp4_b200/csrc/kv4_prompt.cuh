@@ -304,17 +304,13 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
                 tc_fence_after();
                 const uint64_t v = dV + (now & 3) * 1024;
                 const uint32_t tO = tbase + L::T_O + u * 128;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)           // O_u += P_u V
-                  mma_f16_ta_elect(tO, tS + kk * 8, v + kk * 2, idesc_pv, (x == 0 && kk == 0) ? 0u : 1u);
+                mma_f16_ta_k64_elect(tO, tS, v, idesc_pv, x == 0 ? 0u : 1u);   // O_u += P_u V
                 mma_commit_elect(pv_done + 2 * u + h);
               }
               if (x + 2 < mine) {
                 tc_fence_after();
                 const uint64_t q = dQ + u * 2048, k = dK + (nx & 3) * 1024;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)           // S_u = Q_u K^T
-                  mma_f16_elect(tS, q + (kk >> 2) * 1024 + (kk & 3) * 2, k + (kk >> 2) * 512 + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
+                mma_f16_k128_elect<8192>(tS, q, k, idesc_qk);                  // S_u = Q_u K^T
                 mma_commit_elect(s_full + 2 * u + h);
               }
             }

@@ -15,9 +15,10 @@
 // The key tiles of all items form one line, cut into equal ranges, one a CTA (kv4_range), whatever
 // the lengths and however few the rows; an item that crosses CTAs leaves partials.
 //
-// Roles (512 threads): warp 0 issues the products, warp 1 hands out the work and loads Q (TMA), warps
-// 4-7 decode K and V pages into the tensor cores' 128-byte-swizzled layout, warps 8-11 and 12-15 are the
-// units' softmax.
+// Roles (512 threads): warps 0 and 2 issue the products of unit 0 and 1 (one warp for both left the tensor
+// cores waiting while it waited: 323 us a chunk of 512 tokens at 32512, 293 with two), warp 1 hands out
+// the work and loads Q (TMA), warps 4 and 5 decode K and 6 and 7 V, page by page, into the tensor cores'
+// 128-byte-swizzled layout, warps 8-11 and 12-15 are the units' softmax; warp 3 has none.
 // TMEM (512 columns): S_0, S_1 (two half tiles of 64 keys each; P of a half over its first 32 columns), O_0, O_1. The
 // scores of a half are issued as soon as the product with the P in its place is, so that a unit always has
 // one half's scores waiting while its softmax works on the other's.
@@ -206,20 +207,20 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
   if (threadIdx.x == 0) {
     mbar_init(q_raw, 1);
     mbar_init(q_full, kConvertQ ? 8 : 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(k_full + i, 4);
-      mbar_init(k_empty + i, 1);
+      mbar_init(k_full + i, 2);
+      mbar_init(k_empty + i, 2);
       mbar_init(v_full + i, 2);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, 2);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(pv_done + i, 1);
     }
-    mbar_init(mma_final, 1);
+    mbar_init(mma_final, 2);
     for (int i = 0; i < L::NSEG; ++i) {
       mbar_init(seg_full + i, 1);
-      mbar_init(seg_empty + i, 1 + 1 + 6 + 8);           // products, Q, decoding, softmax
+      mbar_init(seg_empty + i, 2 + 1 + 4 + 8);           // products, Q, decoding, softmax
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -245,7 +246,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
   const int TU = 128 / group;                            // tokens of a unit
   // A wait gives up when it has passed its limit, or when another one has (abort_flag: 1 + its barrier |
   // role << 8); the place is reported at the end.
-  const int role = warp == 0 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
+  const int role = warp < 4 && warp != 1 ? kRoleMma : warp < 8 ? kRoleProducer : kRoleSoftmax;
   auto gave_up = [&](uint64_t* bar, long long t0) -> bool {
     if (clock64() - t0 > kWaitLimitCycles) *abort_flag = 1 + static_cast<int>(bar - bars) + (role << 8);
     return *abort_flag != 0;
@@ -265,8 +266,8 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     return true;
   };
 
-  if (warp < 2) {
-    if (warp == 0) {
+  if (warp < 4) {
+    if ((warp & 1) == 0) {
       // ======================= products =======================
       {
         constexpr uint32_t idesc_qk = idesc_f16(128, 64), idesc_pv = idesc_f16(128, 128);
@@ -275,7 +276,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         const uint64_t dK = make_sdesc(smem_u32(sm + L::OFF_K), 16, 1024, kSw128);
         const uint64_t dV = make_sdesc(smem_u32(sm + L::OFF_V), 16, 1024, kSw128);
         int tile = 0;
-        uint32_t odd = 0;                                // bit u: unit u's tiles so far, odd or even
+        uint32_t odd = 0;                                // the unit's tiles so far, odd or even
         bool ok = true;
         for (int seg = 0;; ++seg) {
           ok = waitw(seg_full + seg % L::NSEG, (seg / L::NSEG) & 1);
@@ -287,37 +288,34 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
           if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
           __syncwarp();
           if (end || !(ok = waitw(q_full, seg & 1))) break;
-          // x counts half tiles. Rounds -2 and -1: the first tile's scores. Round x, unit by unit: the product of
-          // half x with V, and the scores of half x + 2 in its place.
+          // x counts half tiles. Rounds -2 and -1: the first tile's scores. Round x: the product of half x with V,
+          // and the scores of half x + 2 in its place.
+          const int u = warp >> 1, mine = 2 * (u ? mine1 : mine0);
 #pragma unroll 1
-          for (int x = -2; x < 2 * len && ok; ++x) {
+          for (int x = -2; x < 2 * len; ++x) {
             const int h = x & 1, now = 2 * tile + x, nx = now + 2;        // pages of halves x and x + 2
-            if (x + 2 < 2 * len && !(ok = waitw(k_full + (nx & 3), (nx >> 2) & 1))) break;
-            if (x >= 0 && !(ok = waitw(v_full + (now & 3), (now >> 2) & 1))) break;
-#pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-              const int mine = 2 * (u ? mine1 : mine0);
-              const uint32_t tS = tbase + L::T_S + u * 128 + h * 64;
-              if (x >= 0 && x < mine) {
-                if (!(ok = waitw(p_full + 2 * u + h, (odd >> u) & 1))) break;
-                odd ^= static_cast<uint32_t>(h) << u;
+            const uint32_t tS = tbase + L::T_S + u * 128 + h * 64;
+            if (x >= 0) {
+              if (!(ok = waitw(v_full + (now & 3), (now >> 2) & 1))) break;
+              if (x < mine) {
+                if (!(ok = waitw(p_full + 2 * u + h, odd))) break;
+                odd ^= h;
                 tc_fence_after();
-                const uint64_t v = dV + (now & 3) * 1024;
-                const uint32_t tO = tbase + L::T_O + u * 128;
-                mma_f16_ta_k64_elect(tO, tS, v, idesc_pv, x == 0 ? 0u : 1u);   // O_u += P_u V
+                mma_f16_ta_k64_elect(tbase + L::T_O + u * 128, tS, dV + (now & 3) * 1024, idesc_pv, x == 0 ? 0u : 1u);   // O_u += P_u V
                 mma_commit_elect(pv_done + 2 * u + h);
               }
+              mma_commit_elect(v_empty + (now & 3));
+            }
+            if (x + 2 < 2 * len) {
+              if (!(ok = waitw(k_full + (nx & 3), (nx >> 2) & 1))) break;
               if (x + 2 < mine) {
                 tc_fence_after();
-                const uint64_t q = dQ + u * 2048, k = dK + (nx & 3) * 1024;
-                mma_f16_k128_elect<8192>(tS, q, k, idesc_qk);                  // S_u = Q_u K^T
+                mma_f16_k128_elect<8192>(tS, dQ + u * 2048, dK + (nx & 3) * 1024, idesc_qk);                  // S_u = Q_u K^T
                 mma_commit_elect(s_full + 2 * u + h);
               }
+              mma_commit_elect(k_empty + (nx & 3));
+              if (x + 3 == 2 * len) mma_commit_elect(q_empty);
             }
-            if (!ok) break;
-            if (x + 2 < 2 * len) mma_commit_elect(k_empty + (nx & 3));
-            if (x + 3 == 2 * len) mma_commit_elect(q_empty);
-            if (x >= 0) mma_commit_elect(v_empty + (now & 3));
           }
           if (!ok) break;
           tile += len;
@@ -366,7 +364,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     __syncwarp();
   } else if (warp < 8) {
     // ============================ K and V decoding ============================
-    // Warps 2 to 5 decode K, warps 6 and 7 V, page by page into rings of four. Codes and scales come
+    // Warps 4 and 5 decode K, warps 6 and 7 V, page by page into rings of four. Codes and scales come
     // two pages ahead, by asynchronous copies that each thread makes for itself; the page's id has been
     // read a page before that. A page that does not exist leaves what was there (codes are always
     // finite) and counts with scale 0. (Loops stay loops: with all roles unrolled the code of a tile
@@ -407,13 +405,13 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     // there are in all, known at the end. Three rounds without a page fill the pipeline.
     Page p0 = {-1, 0, 0}, p1 = p0, p2 = p0;
     int have = 0;                                        // pages handed out so far
-    const int tid = is_v ? (threadIdx.x & 63) : threadIdx.x - 64;
-    // K: a thread has half the channels of a row: eight words of eight channels become eight 16-byte
+    const int tid = threadIdx.x & 63;
+    // K: a thread has half the channels of two rows: eight words of eight channels become eight 16-byte
     // chunks, four at a time. The threads of the upper half begin with the last four, so that the eight threads
     // of four rows write to eight different banks of 16 bytes.
     // V: a thread has eight tokens of 16 channels: four token pairs of a channel are a chunk.
     const int kr = tid >> 1, kh = tid & 1, vt = tid & 7, vb = tid >> 3;
-    unsigned char* codes = sm + L::OFF_CODES + (is_v ? 9216 : 0) + tid * 16;   // K: [slot][2][128], V: [slot][4][64]
+    unsigned char* codes = sm + L::OFF_CODES + (is_v ? 9216 : 0) + tid * 16;   // [slot][4][64]
     unsigned char* scales = sm + L::OFF_CODES + 8192 + (is_v ? 9216 + tid * 8 : tid * 4);
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? v_empty : k_empty;
@@ -434,11 +432,11 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
           }
           unsigned char* row = sm + L::OFF_K + stg * 16384 + kh * 8192 + kr * 128;
 #pragma unroll 1
-          for (int it = 0; it < 2; ++it) {
-            const int o = it ^ kh;                       // which four of the row's words
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + slot * 512 + o * 2);
+          for (int it = 0; it < 4; ++it) {               // rows kr and kr + 32
+            const int o = (it & 1) ^ kh, r = it >> 1;    // which four of the row's words
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + slot * 512 + r * 256 + o * 2);
             const __half2 s2 = e4m3x2_to_half2(there ? sc : 0u);
-            const uint4 c = *reinterpret_cast<const uint4*>(codes + slot * 4096 + o * 2048);
+            const uint4 c = *reinterpret_cast<const uint4*>(codes + slot * 4096 + (r * 2 + o) * 1024);
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
             const uint32_t pos = static_cast<uint32_t>(((kr & 7) << 4) ^ (o << 6));
 #pragma unroll
@@ -448,7 +446,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
               e2m1x8_to_half2(w[e], d);
 #pragma unroll
               for (int x = 0; x < 4; ++x) d[x] = hmul2(d[x], f);
-              *reinterpret_cast<uint4*>(row + (pos ^ (e << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
+              *reinterpret_cast<uint4*>(row + r * 4096 + (pos ^ (e << 4))) = make_uint4(d[0], d[1], d[2], d[3]);
             }
           }
         } else {
@@ -485,9 +483,12 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         const int64_t head = static_cast<int64_t>(p2.id) * a.c.Hkv + p2.h;
         if (!is_v) {
           const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32;
-          cp_async16(codes + slot * 4096, k);
-          cp_async16(codes + slot * 4096 + 2048, k + 16);
-          cp_async4(scales + slot * 512, a.c.k_scales + head * 512 + kr * 8 + kh * 4, true);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            cp_async16(codes + slot * 4096 + r * 2048, k + r * 2048);
+            cp_async16(codes + slot * 4096 + r * 2048 + 1024, k + r * 2048 + 16);
+            cp_async4(scales + slot * 512 + r * 256, a.c.k_scales + head * 512 + (kr + r * 32) * 8 + kh * 4, true);
+          }
         } else {
           const uint8_t* v = a.c.v_pages + head * 4096 + vt * 512 + vb * 16;
 #pragma unroll

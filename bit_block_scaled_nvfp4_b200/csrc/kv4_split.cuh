@@ -1,4 +1,4 @@
-// Attention of few query rows per KV head over the 4-bit cache (decoding steps, proposed tokens):
+// Attention of few query rows per KV head over the 4-bit cache (decoding steps, two tokens of few heads):
 // split over the keys, plus the merge of the splits.
 //
 // Mathematics: for the n query tokens of a sequence and one KV head, the R = n g rows (token,
@@ -171,9 +171,10 @@ struct Kv4Walk {
   }
 };
 
+// NT: tiles of eight rows, 1 or 2.
 template <int NT>
 struct Kv4SplitLayout {
-  static constexpr int WARPS = NT == 4 ? 8 : 12, THREADS = WARPS * 32;
+  static constexpr int WARPS = 12, THREADS = WARPS * 32;
   static constexpr int NS = 2;                          // stages a warp, of one page
   static constexpr int MT = NT == 1 ? 4 : 2;            // tiles of 16 tokens taken at once
   static constexpr int ROWS = NT * 8;
@@ -189,7 +190,7 @@ struct Kv4SplitLayout {
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(8 * M_LD * 4 <= STAGE, "a stage holds a warp's O of eight rows");
 };
-constexpr int kKv4PartRows = 32;                        // rows of a partial (the largest layout's)
+constexpr int kKv4PartRows = 16;                        // rows of a partial (the larger layout's)
 constexpr int kKv4PartFloats = kKv4PartRows * (kKv4D + 2);
 
 // 16-byte asynchronous copy past L1.
@@ -325,15 +326,13 @@ kv4_split_kernel(Kv4AttnArgs a) {
     }
     __syncthreads();
     // a thread's rows of a tile: 2 t and 2 t + 1, in the halves of its pairs
-    uint32_t q[NT <= 2 ? NT : 1][16];
-    if constexpr (NT <= 2) {
+    uint32_t q[NT][16];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          reinterpret_cast<uint4*>(q[nt])[k] =
-              *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + k * 16);
-    }
+      for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint4*>(q[nt])[k] =
+            *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + k * 16);
     float2 m[NT], l[NT];
     float o[NT][8][4];
 #pragma unroll
@@ -377,14 +376,8 @@ kv4_split_kernel(Kv4AttnArgs a) {
               const uint32_t a0[4] = {ha[0], hb[0], ha[1], hb[1]}, a1[4] = {ha[2], hb[2], ha[3], hb[3]};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if constexpr (NT <= 2) {
-                  mma16816(s[mt][nt], a0, q[nt][4 * w], q[nt][4 * w + 1]);
-                  mma16816(s[mt][nt], a1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
-                } else {
-                  const uint4 qq = *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + w * 16);
-                  mma16816(s[mt][nt], a0, qq.x, qq.y);
-                  mma16816(s[mt][nt], a1, qq.z, qq.w);
-                }
+                mma16816(s[mt][nt], a0, q[nt][4 * w], q[nt][4 * w + 1]);
+                mma16816(s[mt][nt], a1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
               }
             }
           }

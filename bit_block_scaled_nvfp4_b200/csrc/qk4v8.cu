@@ -861,17 +861,19 @@ struct Kv4Schedule {
   int split_ctas, prompt_ctas;
   size_t part_off, prompt_plan_off, prompt_part_off, bytes;   // workspace: plan and partials of each
 };
-// Where every sequence has at most 32 rows a KV head (query tokens times heads a group) the split
-// kernel takes them all. Otherwise it takes the sequences of one token (of a whole tile of rows,
-// to be exact), and the prompt kernel the others; a lone sequence is then the prompt kernel's
-// whatever its length, which saves the split kernel's two launches.
+// Where every sequence has at most 16 rows a KV head (query tokens times heads a group) the split
+// kernel takes them all: 24 sequences of 2 tokens x 8 heads a group at 700 to 9000 cached take 95 us, by
+// the prompt kernel 120. From 17 rows on the prompt kernel is the faster one (an instance of the split
+// kernel for 32 rows: 3 tokens 142 us against 122, 128 short sequences 180 against 84, two short ones 29
+// against 31). It then leaves the sequences of one token (of a whole tile of rows, to be exact) to the split kernel;
+// a lone sequence is the prompt kernel's whatever its length, which saves the other's two launches.
 Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
   Kv4Schedule s;
   const int64_t group = p->q_heads / p->cache.kv_heads, rows = p->max_q * group;
-  s.prompt = rows > 32;
+  s.prompt = rows > 16;
   s.split = !s.prompt || p->num_seqs > 1;
   const int64_t r = s.prompt ? group : rows;
-  s.nt = r <= 8 ? 1 : r <= 16 ? 2 : 4;
+  s.nt = r <= 8 ? 1 : 2;
   s.rows_max = s.split ? 8 * s.nt : 0;
   const int64_t heads = static_cast<int64_t>(p->num_seqs) * p->cache.kv_heads, sms = sm_count();
   auto ctas = [&](int64_t units, int64_t least) {
@@ -941,9 +943,8 @@ template <typename T>
 qk4v8_status launch_kv4_attn(const qk4v8_kv4_attn_params* p, const Kv4Schedule& sc, const Kv4AttnArgs& a,
                              cudaStream_t stream) {
   if (sc.split) {
-    const qk4v8_status st = sc.nt == 1   ? launch_kv4_split<1, T>(a, sc.split_ctas, stream)
-                            : sc.nt == 2 ? launch_kv4_split<2, T>(a, sc.split_ctas, stream)
-                                         : launch_kv4_split<4, T>(a, sc.split_ctas, stream);
+    const qk4v8_status st = sc.nt == 1 ? launch_kv4_split<1, T>(a, sc.split_ctas, stream)
+                                         : launch_kv4_split<2, T>(a, sc.split_ctas, stream);
     if (st != QK4V8_OK) return st;
     const dim3 grid(static_cast<unsigned>(p->num_seqs * p->cache.kv_heads), static_cast<unsigned>(sc.rows_max));
     kv4_merge_kernel<T><<<grid, 128, 0, stream>>>(a);

@@ -514,7 +514,10 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
       if (g.s < 0) break;
       const int mine = unit == 0 ? g.mine0 : g.mine1;
       const int t0 = g.tok + unit * TU;
-      float C = *a.c.k_ts * a.softmax_scale * kLog2e;
+      // (rows that are nobody's, with another sequence's Q or none: factor 0, so that they never raise the
+      // maximum and what they hold does not show in the rounding of the warp's others)
+      const bool somebodys = row < TU * group && t0 + row_map[row].x < g.n;
+      float C = somebodys ? *a.c.k_ts * a.softmax_scale * kLog2e : 0.f;
       if constexpr (kConvertQ) {
         // the thread's row of Q to fp16 under a power of two (kv4_row_factor), which goes into its C
         if (!waitw(q_raw, seg & 1)) break;

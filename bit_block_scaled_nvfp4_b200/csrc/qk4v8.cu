@@ -798,7 +798,7 @@ static qk4v8_status check_kv4_cache(const qk4v8_kv4_cache& c) {
   if (!c.k_pages || !c.k_page_scales || !c.k_tensor_scale || !c.v_pages || !c.v_page_scales || !c.v_tensor_scale)
     return QK4V8_ERR_INVALID_ARG;
   if (c.num_pages <= 0 || c.kv_heads <= 0) return QK4V8_ERR_INVALID_ARG;
-  if (c.head_dim != kKv4D) return QK4V8_ERR_UNSUPPORTED;
+  if (c.head_dim != kKv4D || c.kv_heads > 65535) return QK4V8_ERR_UNSUPPORTED;   // (heads: 32-bit indexes of blocks)
   if (!aligned(c.k_pages, 16) || !aligned(c.k_page_scales, 16) || !aligned(c.v_pages, 16) ||
       !aligned(c.v_page_scales, 16) || !aligned(c.k_tensor_scale, 4) || !aligned(c.v_tensor_scale, 4))
     return QK4V8_ERR_INVALID_ARG;
@@ -894,7 +894,8 @@ Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
 }
 
 qk4v8_status check_kv4_attn(const qk4v8_kv4_attn_params* p) {
-  if (p == nullptr || !p->q || !p->context_lens || !p->page_table || !p->out) return QK4V8_ERR_INVALID_ARG;
+  if (p == nullptr || !p->context_lens || !p->page_table) return QK4V8_ERR_INVALID_ARG;
+  if (p->total_q > 0 && (!p->q || !p->out)) return QK4V8_ERR_INVALID_ARG;
   if (const qk4v8_status st = check_kv4_cache(p->cache); st != QK4V8_OK) return st;
   if (p->dtype != QK4V8_F16 && p->dtype != QK4V8_BF16) return QK4V8_ERR_INVALID_ARG;
   if (p->total_q < 0 || p->num_seqs <= 0 || p->max_pages <= 0 || p->q_heads <= 0 || p->max_q <= 0 ||

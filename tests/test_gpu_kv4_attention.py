@@ -2,7 +2,9 @@
 
 Tolerance, element by element, from the arithmetic: with w the weights, A = sum_j w_j |v_j| and
 B = max_j scale * sum_c |q_c k_jc| of the row,
-  * the weights are rounded to fp16, half a step of 2^-10: at most 2^-11 A;
+  * the weights are rounded to fp16, half a step of 2^-10: at most 2^-11 A; as P = 2^(s - m + 6) with m at
+    most the row's maximum, its largest is at least 2^6, and one below 2^-14 is rounded to half a step
+    of 2^-24: 2^-31 of the largest weight at most, each: 2^-31 max w sum_j |v_j|;
   * a score is 128 products summed in float32 by the tensor cores and scaled: at most
     136 * 2^-23 B off, numerator and denominator each: 2 * 136 * 2^-23 B A;
   * exponentials (2 ulp), sums, rescaling and the splits' joining: within 2^-18 A;
@@ -87,6 +89,7 @@ class Case:
                 ref, a = w @ vh, w @ vh.abs()
                 b = ((q.abs() @ kh.abs().T) * scale).masked_fill(~seen, 0).amax(-1, keepdim=True)
                 tol = eps * ref.abs() + (2.0 ** -11 + 2 * 136 * 2.0 ** -23 * b + 2.0 ** -18) * a
+                tol += 2.0 ** -31 * w.amax(-1, keepdim=True) * (seen.double() @ vh.abs())
                 got = out[self.cu[s]:self.cu[s + 1], h].double()
                 d = (got - ref).abs()
                 assert (d <= tol).all(), f"seq {s} head {h}: {float((d / tol).max()):.2f} of the tolerance at {int((d / tol).argmax())}"

@@ -26,6 +26,18 @@ def _stream():
     return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _launch(name: str, dev: int, *args) -> None:
+    """One call of the library on device ``dev`` and its current stream (entering the device costs more
+    than many a call's own checks, so only when it is not the current one)."""
+    fn, stream = getattr(_lib.load(), name), torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    _lib.check(st, name)
+
+
 def _dtype(t: torch.Tensor) -> int:
     if t.dtype not in _DT:
         raise TypeError(f"expected fp16 or bf16, got {t.dtype}")
@@ -38,7 +50,7 @@ def _dtype(t: torch.Tensor) -> int:
 def _expect(t, name: str, shape, dtype) -> None:
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -55,10 +67,14 @@ def _expect_scalar(t, name: str) -> None:
 
 
 def _on_one_gpu(*ts) -> None:
-    ts = [t for t in ts if t is not None]
-    dev = ts[0].get_device()
+    dev = None
     for t in ts:
-        if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
+        if t is None:
+            continue
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if not t.is_cuda or d != dev or not t.is_contiguous():
             raise ValueError("the library takes contiguous tensors on one CUDA device")
 
 
@@ -617,8 +633,7 @@ def kv4_append_paged(cache: PagedKV4, k_new: torch.Tensor, v_new: torch.Tensor, 
     [S, max_pages] int32."""
     _dtype(k_new)
     p = _kv4_tokens(cache, k_new, v_new, cu_new, lens, page_table)
-    with torch.cuda.device(lens.device):
-        _lib.check(_lib.load().kv4_append_paged(C.byref(p), _stream()), "kv4_append_paged")
+    _launch("kv4_append_paged", lens.get_device(), C.byref(p))
 
 
 def kv4_read_paged(cache: PagedKV4, cu: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor,
@@ -637,8 +652,7 @@ def kv4_read_paged(cache: PagedKV4, cu: torch.Tensor, start: torch.Tensor, page_
         if k.shape[0] != total or k.dtype != dtype:
             raise ValueError(f"out: expected {total} rows of {dtype}")
     p = _kv4_tokens(cache, k, v, cu, start, page_table)
-    with torch.cuda.device(start.device):
-        _lib.check(_lib.load().kv4_read_paged(C.byref(p), _stream()), "kv4_read_paged")
+    _launch("kv4_read_paged", start.get_device(), C.byref(p))
     return k, v
 
 
@@ -705,9 +719,8 @@ def attn_kv4_paged(q: torch.Tensor, cache: PagedKV4, page_table: torch.Tensor,
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if want_lse else None
     p = _kv4_attn_params(q, cache, page_table, context_lens, max_context, cu_q, max_q,
                          softmax_scale, out, lse)
-    with torch.cuda.device(dev):
-        ws = _kv4_workspace(p, workspace, dev)
-        _lib.check(_lib.load().attn_kv4_paged(C.byref(p), _ptr(ws), ws.numel(), _stream()), "attn_kv4_paged")
+    ws = _kv4_workspace(p, workspace, dev)
+    _launch("attn_kv4_paged", q.get_device(), C.byref(p), _ptr(ws), ws.numel())
     return (out, lse) if want_lse else out
 
 
@@ -754,12 +767,7 @@ class KV4AttentionPlan:
                 raise ValueError("cu_q must be contiguous on the plan's device")
             p.cu_q = cu_q.data_ptr()
         p.q, p.q_stride, p.total_q = q.data_ptr(), _token_stride(q, "q"), T
-        if torch.cuda.current_device() == self._dev:
-            st = _lib.load().attn_kv4_paged(C.byref(p), _ptr(self.workspace), self.workspace.numel(), _stream())
-        else:
-            with torch.cuda.device(self._dev):
-                st = _lib.load().attn_kv4_paged(C.byref(p), _ptr(self.workspace), self.workspace.numel(), _stream())
-        _lib.check(st, "attn_kv4_paged")
+        _launch("attn_kv4_paged", self._dev, C.byref(p), _ptr(self.workspace), self.workspace.numel())
         return (self.out[:T], self.lse[:T]) if self.lse is not None else self.out[:T]
 
 
@@ -803,9 +811,7 @@ def kv_pages_alloc(pool, page_table: torch.Tensor, lens: torch.Tensor, new_lens:
     if new_lens.numel() != lens.numel():
         raise ValueError("new_lens must have one entry per sequence")
     ws = _pool_workspace(pool, page_table)
-    with torch.cuda.device(lens.device):
-        _lib.check(_lib.load().kv_pages_alloc(*args, _ptr(new_lens), _ptr(ws), ws.numel(), _stream()),
-                   "kv_pages_alloc")
+    _launch("kv_pages_alloc", lens.get_device(), *args, _ptr(new_lens), _ptr(ws), ws.numel())
 
 
 def kv_pages_fork(pool, page_table: torch.Tensor, lens: torch.Tensor, src: torch.Tensor,
@@ -818,11 +824,8 @@ def kv_pages_fork(pool, page_table: torch.Tensor, lens: torch.Tensor, src: torch
     if dst.numel() != n:
         raise ValueError("src and dst must have the same number of sequences")
     ws = _pool_workspace(pool, page_table)
-    with torch.cuda.device(lens.device):
-        m = torch.empty(4, n, dtype=torch.int32, device=lens.device)
-        _lib.check(_lib.load().kv_pages_fork(*args, _ptr(src), _ptr(dst), n, _ptr(m[0]), _ptr(m[1]),
-                                             _ptr(m[2]), _ptr(m[3]), _ptr(ws), ws.numel(), _stream()),
-                   "kv_pages_fork")
+    m = torch.empty(4, n, dtype=torch.int32, device=lens.device).unbind()
+    _launch("kv_pages_fork", lens.get_device(), *args, _ptr(src), _ptr(dst), n, *map(_ptr, m), _ptr(ws), ws.numel())
     return PageMoves(m[0], m[1], pool.refs.numel(), None, m[2], m[3])
 
 
@@ -830,8 +833,7 @@ def kv_pages_free(pool, page_table: torch.Tensor, lens: torch.Tensor, seqs: torc
     """Drop the sequences seqs[i] (int32 device tensor): their pages' counts fall, their table
     entries become -1 and their lengths 0."""
     args = _pool_args(pool, page_table, lens, ("seqs", seqs))
-    with torch.cuda.device(lens.device):
-        _lib.check(_lib.load().kv_pages_free(*args, _ptr(seqs), seqs.numel(), _stream()), "kv_pages_free")
+    _launch("kv_pages_free", lens.get_device(), *args, _ptr(seqs), seqs.numel())
 
 
 def kv_pages_compact(pool, page_table: torch.Tensor, lens: torch.Tensor) -> PageMoves:
@@ -841,22 +843,18 @@ def kv_pages_compact(pool, page_table: torch.Tensor, lens: torch.Tensor) -> Page
     args = _pool_args(pool, page_table, lens)
     P = pool.refs.numel()
     ws = _pool_workspace(pool, page_table)
-    with torch.cuda.device(lens.device):
-        m = torch.empty(2 * (P // 2 + 1) + 1, dtype=torch.int32, device=lens.device)
-        src, dst, count = m[:P // 2 + 1], m[P // 2 + 1:-1], m[-1:]
-        _lib.check(_lib.load().kv_pages_compact(*args, _ptr(src), _ptr(dst), _ptr(count), _ptr(ws),
-                                                ws.numel(), _stream()), "kv_pages_compact")
+    half = P // 2 + 1
+    src, dst, count = torch.empty(2 * half + 1, dtype=torch.int32, device=lens.device).split((half, half, 1))
+    _launch("kv_pages_compact", lens.get_device(), *args, _ptr(src), _ptr(dst), _ptr(count), _ptr(ws), ws.numel())
     return PageMoves(src, dst, P, count)
 
 
-def _copy_rows(arrays, src, dst, rows: int, count, where: str) -> None:
+def _copy_rows(arrays, src, dst, rows: int, count) -> None:
     _on_one_gpu(*arrays, src, dst, count)
     n = len(arrays)
     ptrs = (C.c_void_p * n)(*[a.data_ptr() for a in arrays])
     size = (C.c_int64 * n)(*[a.numel() // rows * a.element_size() for a in arrays])
-    with torch.cuda.device(src.device):
-        _lib.check(_lib.load().kv_pages_copy(ptrs, size, n, rows, _ptr(src), _ptr(dst), src.numel(),
-                                             _ptr(count), _stream()), where)
+    _launch("kv_pages_copy", src.get_device(), ptrs, size, n, rows, _ptr(src), _ptr(dst), src.numel(), _ptr(count))
 
 
 def kv_pages_copy(cache, moves: PageMoves) -> None:
@@ -865,7 +863,7 @@ def kv_pages_copy(cache, moves: PageMoves) -> None:
     for a in arrays:
         if a.shape[0] != moves.num_pages:
             raise ValueError(f"the cache has {a.shape[0]} pages, the moves are of {moves.num_pages}")
-    _copy_rows(arrays, moves.src, moves.dst, moves.num_pages, moves.count, "kv_pages_copy")
+    _copy_rows(arrays, moves.src, moves.dst, moves.num_pages, moves.count)
 
 
 def kv_tails_copy(v_tail: torch.Tensor, moves: PageMoves) -> None:
@@ -873,7 +871,7 @@ def kv_tails_copy(v_tail: torch.Tensor, moves: PageMoves) -> None:
     [S, Hkv, D, 32] of a PagedKV), copied to the sequences forked into."""
     if moves.seq_src is None:
         raise ValueError("moves of a fork are needed")
-    _copy_rows([v_tail], moves.seq_src, moves.seq_dst, v_tail.shape[0], None, "kv_tails_copy")
+    _copy_rows([v_tail], moves.seq_src, moves.seq_dst, v_tail.shape[0], None)
 
 
 def qk4v8_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,

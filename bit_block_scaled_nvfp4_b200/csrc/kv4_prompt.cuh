@@ -30,17 +30,26 @@ namespace qk4v8 {
 constexpr float kRiseLimit = 8.f;                        // log2 of how far the maximum may rise unfollowed
 constexpr int kPromptPartFloats = 256 * (kKv4D + 2);     // a partial: O, then m, then l of 256 rows
 
-// sum over i < n of floor((a i + b) / 128)
-__device__ __forceinline__ int64_t floor_sum128(int64_t n, int64_t a, int64_t b) {
-  int64_t m = 128, ans = 0;
+// sum over i < n of floor((a i + b) / 128), n < 2^31, by the steps of Euclid's algorithm on (a, 128). Divisions are in
+// 32 bits where the numbers allow it: 64-bit ones made the search for a CTA's place take 10 us.
+__device__ __forceinline__ int64_t floor_sum128(uint32_t n, uint32_t a, uint64_t b64) {
+  uint32_t m = 128, b = static_cast<uint32_t>(b64 & 127);
+  int64_t ans = static_cast<int64_t>(n) * static_cast<int64_t>(b64 >> 7);
   while (true) {
-    if (a >= m) { ans += (n - 1) * n / 2 * (a / m); a %= m; }
-    if (b >= m) { ans += n * (b / m); b %= m; }
-    const int64_t y = a * n + b;
+    const uint32_t q = a / m;
+    a -= q * m;
+    ans += static_cast<int64_t>(n) * (n - 1) / 2 * q + static_cast<int64_t>(n) * (b / m);
+    b %= m;
+    const uint64_t y = static_cast<uint64_t>(a) * n + b;
     if (y < m) return ans;
-    n = y / m;
-    b = y % m;
-    const int64_t t = m;
+    if (y >> 32) {
+      n = static_cast<uint32_t>(y / m);
+      b = static_cast<uint32_t>(y % m);
+    } else {
+      n = static_cast<uint32_t>(y) / m;
+      b = static_cast<uint32_t>(y) - n * m;
+    }
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -57,7 +66,7 @@ struct PromptSeq {
   __device__ __forceinline__ int64_t before(int i) const {          // units of the items before item i
     const int last = items();
     const int64_t k = i < last ? i : last - 1;
-    const int64_t s = k > 0 ? floor_sum128(k, T2, static_cast<int64_t>(q.ctx - q.n) + T2 + 127) : 0;
+    const int64_t s = k > 0 ? floor_sum128(static_cast<uint32_t>(k), T2, static_cast<uint64_t>(q.ctx - q.n) + T2 + 127) : 0;
     return i + (i < last ? s : s + tiles(last - 1));
   }
 };
@@ -70,6 +79,12 @@ struct PromptSeg {
   int mine0, mine1;                                      // how many of them unit 0 and 1 see
   int whole, first;                                      // the whole item; it begins here
 };                                                       // (s = -1: no more)
+// Where a CTA's range begins inside an item: for the kernel that joins the partials.
+struct PromptCut {
+  int j, units;                                          // units of the item before the range (0: no cut), in all
+  int tok, h, q0, n;                                     // its first token, KV head; its sequence's first row, tokens
+  int pad[2];
+};
 struct PromptLayout {
   static constexpr int OFF_Q = 0;                        // [unit] 2 x 16 KB (64 channels each)
   static constexpr int OFF_K = 65536;                    // [4] pages, 2 x 8 KB (64 channels each)
@@ -200,7 +215,10 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
 
   uchar2* row_map = reinterpret_cast<uchar2*>(sm + L::OFF_MAP);
   if ((smem_u32(sm) & 1023u) != 0) {                     // cannot happen; the tensor cores would read other rows
-    if (threadIdx.x == 0) flag_error(kStatusBounds);
+    if (threadIdx.x == 0) {
+      flag_error(kStatusBounds);
+      a.prompt_cut[blockIdx.x] = {};
+    }
     return;
   }
   if (threadIdx.x < 128) row_map[threadIdx.x] = make_uchar2(threadIdx.x / group, threadIdx.x % group);
@@ -340,6 +358,12 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         ++handed;
       };
       walk->start(a, rng);
+      {
+        PromptCut cut = {};
+        if (walk->left > 0 && walk->j > 0)
+          cut = {walk->j, walk->sq.units(walk->i), walk->i * walk->sq.T2, walk->h, walk->sq.q.q0, walk->sq.q.n, {0, 0}};
+        a.prompt_cut[blockIdx.x] = cut;
+      }
       hand_out();
       hand_out();
       int seg = 0;
@@ -689,63 +713,43 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
   }
 }
 
-// Joins the partials of items that cross CTAs. CTA (i, y) takes the item that CTA i - 1 of the prompt
-// kernel began and CTA i went on with, if any, and rows 32 y ..; a warp takes four rows, a lane four
+// Joins the partials of items that cross CTAs. CTA (i, y) takes the item that CTA i of the prompt
+// kernel began and CTA i + 1 went on with, if any, and rows 8 y ..; a warp takes a row, a lane four
 // channels.
 template <typename T>
 __global__ void __launch_bounds__(256) kv4_prompt_merge_kernel(Kv4AttnArgs a) {
-  const int cta = blockIdx.x + 1, group = a.Hq / a.c.Hkv;
-  const int64_t per = a.prompt_plan[0], at = per * cta;
-  int lo = 0, hi = a.S - 1;                              // the last sequence that begins at or before `at`
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (a.prompt_plan[1 + m] <= at) lo = m; else hi = m - 1;
-  }
-  PromptSeq sq;
-  sq.T2 = 2 * (128 / group);
-  sq.q = kv4_seq(a, lo, false);
-  if (sq.q.n * group <= a.rows_max) return;              // `at` is behind the last unit
-  const int64_t head = sq.before(sq.items()), in = at - a.prompt_plan[1 + lo];
-  const int h = static_cast<int>(in / head);
-  if (h >= a.c.Hkv) return;
-  const int64_t r = in - h * head;
-  int i0 = 0, i1 = sq.items() - 1;
-  while (i0 < i1) {
-    const int m = (i0 + i1 + 1) >> 1;
-    if (sq.before(m) <= r) i0 = m; else i1 = m - 1;
-  }
-  const int64_t first = at - (r - sq.before(i0));        // the item's first unit
-  if (first == at || first / per != cta - 1) return;     // not cut here, or not here first
-  const int c1 = static_cast<int>((first + sq.units(i0) - 1) / per);
+  const int cta = blockIdx.x + 1, group = a.Hq / a.c.Hkv, TU = 128 / group;
+  const PromptCut cut = a.prompt_cut[cta];
+  const int per = static_cast<int>(a.prompt_plan[0]);    // units a CTA
+  if (cut.j == 0 || cut.j > per) return;                 // not cut here, or not here first
+  const int c1 = cta + (cut.units - cut.j - 1) / per;
   // (a first unit alone at the end of a CTA's range has left no partial)
-  const int c0 = at - first == 1 ? cta : cta - 1;
+  const int c0 = cut.j == 1 ? cta : cta - 1;
   if (c0 == c1) return;                                  // written by the prompt kernel
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, TU = sq.T2 / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto part = [&](int c) {
     return a.prompt_part + static_cast<int64_t>(2 * c + (c == cta - 1 ? 1 : 0)) * kPromptPartFloats;
   };
-  for (int k = 0; k < 4; ++k) {
-    const int row = blockIdx.y * 32 + warp * 4 + k, ru = row & 127;
-    const int tok = i0 * sq.T2 + (row >> 7) * TU + ru / group;
-    if (ru >= TU * group || tok >= sq.q.n) continue;
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, part(c)[256 * kKv4D + row]);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = part(c);
-      const float w = ex2_approx(p[256 * kKv4D + row] - mu);
-      const float4 v = *reinterpret_cast<const float4*>(p + row * kKv4D + lane * 4);
-      l += w * p[256 * (kKv4D + 1) + row];
-      acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
-    }
-    const float f = l == 0.f ? 0.f : *a.c.v_ts / l;
-    const int64_t orow = static_cast<int64_t>(sq.q.q0 + tok) * a.Hq + h * group + ru % group;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * kKv4D + lane * 4) =
-        make_uint2(pack2<T>(acc.x * f, acc.y * f), pack2<T>(acc.z * f, acc.w * f));
-    if (a.lse != nullptr && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l) - kPShift) * kLn2;
+  const int row = blockIdx.y * 8 + warp, ru = row & 127;
+  const int tok = cut.tok + (row >> 7) * TU + ru / group;
+  if (ru >= TU * group || tok >= cut.n) return;
+  float M = -INFINITY;
+  for (int c = c0; c <= c1; ++c) M = fmaxf(M, part(c)[256 * kKv4D + row]);
+  const float mu = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; ++c) {
+    const float* p = part(c);
+    const float w = ex2_approx(p[256 * kKv4D + row] - mu);
+    const float4 v = *reinterpret_cast<const float4*>(p + row * kKv4D + lane * 4);
+    l += w * p[256 * (kKv4D + 1) + row];
+    acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
   }
+  const float f = l == 0.f ? 0.f : *a.c.v_ts / l;
+  const int64_t orow = static_cast<int64_t>(cut.q0 + tok) * a.Hq + cut.h * group + ru % group;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * kKv4D + lane * 4) =
+      make_uint2(pack2<T>(acc.x * f, acc.y * f), pack2<T>(acc.z * f, acc.w * f));
+  if (a.lse != nullptr && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l) - kPShift) * kLn2;
 }
 
 }  // namespace qk4v8

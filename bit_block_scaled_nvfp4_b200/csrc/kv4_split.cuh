@@ -38,6 +38,7 @@
 
 namespace qk4v8 {
 
+struct PromptCut;
 struct Kv4AttnArgs {
   Kv4Cache c;
   const void* q;
@@ -53,6 +54,7 @@ struct Kv4AttnArgs {
   int64_t* plan;             // workspace: the split kernel's kv4_range plan
   float* part;               // workspace: its partials, two a CTA
   int64_t* prompt_plan;      // the same of the prompt kernel
+  PromptCut* prompt_cut;   // one a CTA
   float* prompt_part;
 };
 

@@ -859,7 +859,7 @@ struct Kv4Schedule {
   int nt;                 // split kernel: tiles of eight rows
   int rows_max;           // sequences with at most this many rows a KV head go to it, others to the prompt kernel
   int split_ctas, prompt_ctas;
-  size_t part_off, prompt_plan_off, prompt_part_off, bytes;   // workspace: plan and partials of each
+  size_t part_off, prompt_plan_off, prompt_cut_off, prompt_part_off, bytes;   // workspace: plan and partials of each
 };
 // Where every sequence has at most 16 rows a KV head (query tokens times heads a group) the split
 // kernel takes them all: 24 sequences of 2 tokens x 8 heads a group at 700 to 9000 cached take 95 us, by
@@ -887,7 +887,8 @@ Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
   const size_t plan = (8 * (static_cast<size_t>(p->num_seqs) + 1) + 15) / 16 * 16;
   s.part_off = plan;
   s.prompt_plan_off = s.split ? s.part_off + static_cast<size_t>(s.split_ctas) * 2 * kKv4PartFloats * 4 : 0;
-  s.prompt_part_off = s.prompt_plan_off + plan;
+  s.prompt_cut_off = s.prompt_plan_off + plan;
+  s.prompt_part_off = s.prompt_cut_off + static_cast<size_t>(s.prompt_ctas) * sizeof(PromptCut);
   s.bytes = s.prompt ? s.prompt_part_off + static_cast<size_t>(s.prompt_ctas) * 2 * kPromptPartFloats * 4
                      : s.prompt_plan_off;
   return s;
@@ -936,7 +937,7 @@ qk4v8_status launch_kv4_prompt(const Kv4AttnArgs& a, int ctas, cudaStream_t stre
   if (!opt_in.run(current_device(), [] { return set_smem(kv4_prompt_kernel<T>, L::SMEM_ALLOC); })) return QK4V8_ERR_CUDA;
   kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_ALLOC, stream>>>(tq, a);
   if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
-  if (ctas > 1) kv4_prompt_merge_kernel<T><<<dim3(ctas - 1, 8), 256, 0, stream>>>(a);
+  if (ctas > 1) kv4_prompt_merge_kernel<T><<<dim3(ctas - 1, 32), 256, 0, stream>>>(a);
   return launch_status();
 }
 
@@ -975,6 +976,7 @@ extern "C" qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* p, void* wor
   a.plan = reinterpret_cast<int64_t*>(ws);
   a.part = reinterpret_cast<float*>(ws + sc.part_off);
   a.prompt_plan = reinterpret_cast<int64_t*>(ws + sc.prompt_plan_off);
+  a.prompt_cut = reinterpret_cast<PromptCut*>(ws + sc.prompt_cut_off);
   a.prompt_part = reinterpret_cast<float*>(ws + sc.prompt_part_off);
   return p->dtype == QK4V8_BF16 ? launch_kv4_attn<__nv_bfloat16>(p, sc, a, stream)
                                 : launch_kv4_attn<__half>(p, sc, a, stream);

@@ -728,7 +728,8 @@ class KV4AttentionPlan:
     """attn_kv4_paged for serving loops: the fixed buffers (cache, page table, context lengths,
     outputs for up to ``max_tokens`` query tokens, workspace) are checked and allocated once;
     ``run(q, cu_q)`` checks the step's queries and launches, and returns views of the plan's own
-    outputs (read them before the next ``run``)."""
+    outputs (read them before the next ``run``). Steps that may overlap, on two streams or in two
+    graphs, need a plan each: outputs and workspace are the plan's."""
 
     def __init__(self, cache: PagedKV4, page_table: torch.Tensor, context_lens: torch.Tensor,
                  max_context: int, q_heads: int, max_q: int = 1, max_tokens: int | None = None,

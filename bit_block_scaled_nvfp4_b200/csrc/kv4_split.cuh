@@ -31,6 +31,8 @@
 // by 16-byte asynchronous copies, with no barrier between warps until a pair ends. (One warp
 // issuing bulk copies for all of them reached 1 page in 1020 cycles, 4 copies of 4096 + 4096 +
 // 512 + 512 bytes: 33 % of the HBM rate.)
+// Measured: 64 sequences of 8192 to 32768 tokens, 32 query and 8 KV heads, one token each: 273 us with the
+// join, 5.6 TB/s (86 % of the measured 6.5); one sequence of 1001 tokens: 12 us, two launches.
 #pragma once
 #include <type_traits>
 #include "kv4.cuh"

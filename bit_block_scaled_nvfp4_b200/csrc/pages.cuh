@@ -6,6 +6,10 @@
 // The planning steps need one consistent view of refs and lens, so each is one CTA: a pass over
 // refs (4 bytes a page, 64 pages a warp-wide 16-byte load) and block scans. Work that grows with
 // the bytes moved (page contents, page tables) runs over the whole device.
+//
+// Measured on the device: 64 sequences of 200 to 4000 tokens freed and forked again, their last pages copied:
+// 17 us, three launches and the one CTA's passes (the bytes alone: 1.3 us); 48 sequences of 500 to 5000 tokens
+// compacted among three times as many pages, contents of 8 heads copied: 52 us, of which the copies' bytes are 32.
 #pragma once
 #include "ptx.cuh"
 

@@ -497,7 +497,7 @@ static qk4v8_status launch_fwd(const qk4v8_fwd_params* p, cudaStream_t stream) {
     tq16 = tq; tk16 = tk; tv16 = tv;
   }
   static PerDeviceOnce opt_in;                  // one per kernel instance
-  if (!opt_in.run(current_device(), [] { return set_smem(attn_fwd_kernel<D, kMixed, kUA, kDQ>, L::SMEM_ALLOC); }))
+  if (!opt_in.run(current_device(), [] { return set_smem(attn_fwd_kernel<D, kMixed, kUA, kDQ>, L::SMEM_BYTES); }))
     return QK4V8_ERR_CUDA;
   FwdArgs a;
   a.q_scales = p->q_scales; a.k_scales = p->k_scales; a.v_scales = p->v_scales;
@@ -514,7 +514,7 @@ static qk4v8_status launch_fwd(const qk4v8_fwd_params* p, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(a.Tq) * B * Hq;
   if (items > INT32_MAX / 2) return QK4V8_ERR_UNSUPPORTED;
   const int64_t grid = items < sm_count() ? items : sm_count();
-  attn_fwd_kernel<D, kMixed, kUA, kDQ><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_ALLOC, stream>>>(tq, tk, tv, tq16, tk16, tv16, a);
+  attn_fwd_kernel<D, kMixed, kUA, kDQ><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_BYTES, stream>>>(tq, tk, tv, tq16, tk16, tv16, a);
   return launch_status();
 }
 
@@ -544,7 +544,7 @@ static qk4v8_status launch_pp(const qk4v8_fwd_params* p, cudaStream_t stream) {
   static PerDeviceOnce opt_in;
   if (!opt_in.run(current_device(), [] {
         cudaFuncAttributes fa;
-        return set_smem(attn_pp_kernel<D>, L::SMEM_ALLOC) &&
+        return set_smem(attn_pp_kernel<D>, L::SMEM_BYTES) &&
                cudaFuncGetAttributes(&fa, attn_pp_kernel<D>) == cudaSuccess &&
                fa.numRegs == L::REGS_LAUNCH;
       }))
@@ -564,7 +564,7 @@ static qk4v8_status launch_pp(const qk4v8_fwd_params* p, cudaStream_t stream) {
   if (items > INT32_MAX / 2) return QK4V8_ERR_UNSUPPORTED;
   const int64_t n_pairs = pp_items(B, Hq, Hkv, a.Tq);
   const int64_t grid = n_pairs < sm_count() ? n_pairs : sm_count();
-  attn_pp_kernel<D><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_ALLOC, stream>>>(tq, tk, tv, a);
+  attn_pp_kernel<D><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_BYTES, stream>>>(tq, tk, tv, a);
   return launch_status();
 }
 
@@ -911,6 +911,10 @@ qk4v8_status check_kv4_attn(const qk4v8_kv4_attn_params* p) {
   // units of work (a page of a KV head of a sequence) are counted in 32 bits
   const int64_t head_pages = static_cast<int64_t>((p->max_context - 1) / 64 + 1) * p->cache.kv_heads;
   if (head_pages > 0x3fffffff / p->num_seqs) return QK4V8_ERR_UNSUPPORTED;
+  // and so are the prompt kernel's (a tile of 128 keys of an item) in a CTA's range
+  const int64_t items = p->total_q / (2 * (128 / (p->q_heads / p->cache.kv_heads))) + p->num_seqs;
+  if (items > (int64_t{1} << 36) / (static_cast<int64_t>((p->max_context - 1) / 128 + 2) * p->cache.kv_heads))
+    return QK4V8_ERR_UNSUPPORTED;
   return QK4V8_OK;
 }
 
@@ -934,8 +938,8 @@ qk4v8_status launch_kv4_prompt(const Kv4AttnArgs& a, int ctas, cudaStream_t stre
   const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   if (!make_map(&tq, dt, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return QK4V8_ERR_CUDA;
   static PerDeviceOnce opt_in;
-  if (!opt_in.run(current_device(), [] { return set_smem(kv4_prompt_kernel<T>, L::SMEM_ALLOC); })) return QK4V8_ERR_CUDA;
-  kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_ALLOC, stream>>>(tq, a);
+  if (!opt_in.run(current_device(), [] { return set_smem(kv4_prompt_kernel<T>, L::SMEM_BYTES); })) return QK4V8_ERR_CUDA;
+  kv4_prompt_kernel<T><<<ctas, L::THREADS, L::SMEM_BYTES, stream>>>(tq, a);
   if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
   if (ctas > 1) kv4_prompt_merge_kernel<T><<<dim3(ctas - 1, 32), 256, 0, stream>>>(a);
   return launch_status();

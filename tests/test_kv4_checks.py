@@ -187,6 +187,8 @@ def test_attention_validation(lib):
         assert call(**kw) == BAD, kw
     assert call(q_heads=34, q_stride=34 * 128) == UNSUPPORTED                       # 17 heads a group
     assert call(num_seqs=1 << 20, max_pages=1 << 20, max_context=1 << 26) == UNSUPPORTED
+    far = 2 ** 31 - 1                                     # more tiles than a CTA's range can count
+    assert call(num_seqs=1, total_q=far, max_q=far, max_context=far, max_pages=1 << 26) == UNSUPPORTED
     for bad in (dict(ws=0), dict(ws=FAKE + 8), dict(ws_bytes=16)):
         assert call(**bad) == BAD, bad
 

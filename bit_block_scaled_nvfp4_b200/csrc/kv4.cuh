@@ -8,7 +8,7 @@
 // A CTA's 256 threads cover consecutive rows; the first row's sequence is found by counting the
 // offsets not past it (all threads, one pass over cu), later rows walk on from there.
 //
-// Bound: HBM; stored are 512 bytes of K and V in and 144 out a token and head, read back the reverse. 22000
+// Bound: HBM; stored are 512 bytes of K and V in and 144 out a token and head, read back the reverse. 30000
 // tokens of 8 heads stored and read back take 97 us on the device, 3.3 TB/s of 6.5: what is left is the
 // encoder's arithmetic (about 115 instructions a block) and V's scales, one or two bytes a 64-byte row
 // apart. 64 tokens, one a sequence, take 8.4 us for both calls: two launches.

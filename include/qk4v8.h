@@ -488,7 +488,7 @@ typedef struct {
   int32_t max_q;               /* host-side bound on n_s */
   int32_t max_context;         /* host-side bound on context_lens */
   float softmax_scale;
-  void* out;                   /* [total_q, Hq, D] contiguous, 16-byte aligned */
+  void* out;                   /* [total_q, Hq, D] contiguous, 16-byte aligned, apart from q */
   float* lse;                  /* optional [total_q, Hq] natural-log sum-exp; or NULL */
 } qk4v8_kv4_attn_params;
 

@@ -497,7 +497,7 @@ static qk4v8_status launch_fwd(const qk4v8_fwd_params* p, cudaStream_t stream) {
     tq16 = tq; tk16 = tk; tv16 = tv;
   }
   static PerDeviceOnce opt_in;                  // one per kernel instance
-  if (!opt_in.run(current_device(), [] { return set_smem(attn_fwd_kernel<D, kMixed, kUA, kDQ>, L::SMEM_BYTES); }))
+  if (!opt_in.run(current_device(), [] { return set_smem(attn_fwd_kernel<D, kMixed, kUA, kDQ>, L::SMEM_ALLOC); }))
     return QK4V8_ERR_CUDA;
   FwdArgs a;
   a.q_scales = p->q_scales; a.k_scales = p->k_scales; a.v_scales = p->v_scales;
@@ -514,7 +514,7 @@ static qk4v8_status launch_fwd(const qk4v8_fwd_params* p, cudaStream_t stream) {
   const int64_t items = static_cast<int64_t>(a.Tq) * B * Hq;
   if (items > INT32_MAX / 2) return QK4V8_ERR_UNSUPPORTED;
   const int64_t grid = items < sm_count() ? items : sm_count();
-  attn_fwd_kernel<D, kMixed, kUA, kDQ><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_BYTES, stream>>>(tq, tk, tv, tq16, tk16, tv16, a);
+  attn_fwd_kernel<D, kMixed, kUA, kDQ><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_ALLOC, stream>>>(tq, tk, tv, tq16, tk16, tv16, a);
   return launch_status();
 }
 
@@ -544,7 +544,7 @@ static qk4v8_status launch_pp(const qk4v8_fwd_params* p, cudaStream_t stream) {
   static PerDeviceOnce opt_in;
   if (!opt_in.run(current_device(), [] {
         cudaFuncAttributes fa;
-        return set_smem(attn_pp_kernel<D>, L::SMEM_BYTES) &&
+        return set_smem(attn_pp_kernel<D>, L::SMEM_ALLOC) &&
                cudaFuncGetAttributes(&fa, attn_pp_kernel<D>) == cudaSuccess &&
                fa.numRegs == L::REGS_LAUNCH;
       }))
@@ -564,7 +564,7 @@ static qk4v8_status launch_pp(const qk4v8_fwd_params* p, cudaStream_t stream) {
   if (items > INT32_MAX / 2) return QK4V8_ERR_UNSUPPORTED;
   const int64_t n_pairs = pp_items(B, Hq, Hkv, a.Tq);
   const int64_t grid = n_pairs < sm_count() ? n_pairs : sm_count();
-  attn_pp_kernel<D><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_BYTES, stream>>>(tq, tk, tv, a);
+  attn_pp_kernel<D><<<static_cast<unsigned>(grid), L::THREADS, L::SMEM_ALLOC, stream>>>(tq, tk, tv, a);
   return launch_status();
 }
 

@@ -105,13 +105,15 @@ struct PromptLayout {
   static constexpr int N_BARS = 32 + 2 * NSEG;
   static constexpr int OFF_SEG = (OFF_BAR + N_BARS * 8 + 16 + 15) / 16 * 16;
   static constexpr int OFF_WALK = OFF_SEG + NSEG * 64;
-  static constexpr int SMEM_BYTES = OFF_WALK + 64;
+  static constexpr int OFF_NAN = OFF_WALK + 64;          // [NSEG][8] first key with a NaN in these 16 V channels
+  static constexpr int SMEM_BYTES = OFF_NAN + NSEG * 32;
+  static_assert(OFF_NAN % 16 == 0, "reset in words of 16 bytes");
   static_assert(sizeof(PromptSeg) <= 64, "a segment's slot");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static constexpr uint32_t T_S = 0, T_O = 256;          // + 128 for unit 1; S + 64 for a tile's second half
   static constexpr int THREADS = 512;
 };
-struct PromptWalk {
+struct PromptWalk {                                      // (in OFF_WALK's 64 bytes)
   PromptSeq sq;
   int s, h, i, j, left;
   __device__ __forceinline__ void find(const Kv4AttnArgs& a) {
@@ -360,6 +362,8 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
       auto hand_out = [&]() {
         PromptSeg* g = reinterpret_cast<PromptSeg*>(sm + L::OFF_SEG + (handed % L::NSEG) * 64);
         if (!walk->next(a, *g)) g->s = -1;
+        int4* nans = reinterpret_cast<int4*>(sm + L::OFF_NAN + (handed % L::NSEG) * 32);
+        nans[0] = nans[1] = make_int4(INT_MAX, INT_MAX, INT_MAX, INT_MAX);
         mbar_arrive(seg_full + handed % L::NSEG);
         ++handed;
       };
@@ -401,7 +405,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
     // passes the instruction cache, and a decoded word cost five times its instructions.)
     const bool is_v = warp >= 6;
     struct Page {
-      int id, h, left;                                   // -1: none; KV head; slots in the context
+      int id, h, left;                                   // -1: none; KV head, segment's slot << 16; slots in the context
     };
     int seg = -1, pages = 0, seg_h = 0, left = 0;
     const int32_t* ids = nullptr;
@@ -420,7 +424,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         }
         const PromptSeg& g = seg_at(seg);
         pages = 2 * g.len - 1;
-        seg_h = g.h;
+        seg_h = g.h | (seg % L::NSEG) << 16;
         left = g.ctx - g.j0 * 128;
         ids = a.table + static_cast<int64_t>(g.s) * a.max_pages + 2 * g.j0;
       }
@@ -487,6 +491,14 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
             sc.x &= static_cast<uint32_t>(keep);
             sc.y &= static_cast<uint32_t>(keep >> 32);
           }
+          // A NaN would reach the rows that do not see it too (0 x NaN): value 0, and NaN for those that do at the end
+          const uint32_t nx = e4m3_nans(sc.x), ny = e4m3_nans(sc.y);
+          if (nx | ny) {
+            const int at = vt * 8 + (nx ? (__ffs(nx) >> 3) - 1 : (__ffs(ny) >> 3) + 3);
+            atomicMin(reinterpret_cast<int*>(sm + L::OFF_NAN) + (p0.h >> 16) * 8 + vb, at - p0.left);
+            sc.x &= ~((nx >> 7) * 0xFFu);
+            sc.y &= ~((ny >> 7) * 0xFFu);
+          }
           const __half2 f[4] = {e4m3x2_to_half2(sc.x & 0xFFFFu), e4m3x2_to_half2(sc.x >> 16),
                                 e4m3x2_to_half2(sc.y & 0xFFFFu), e4m3x2_to_half2(sc.y >> 16)};
           unsigned char* row = sm + L::OFF_V + stg * 16384 + vb * 16 * 128;
@@ -510,7 +522,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         if (lane == 0) mbar_arrive(full + stg);
       }
       if (valid(p2.id)) {                                // into the place of the page just decoded
-        const int64_t head = static_cast<int64_t>(p2.id) * a.c.Hkv + p2.h;
+        const int64_t head = static_cast<int64_t>(p2.id) * a.c.Hkv + (p2.h & 0xFFFF);
         if (!is_v) {
           const uint8_t* k = a.c.k_pages + head * 4096 + kr * 64 + kh * 32;
 #pragma unroll
@@ -668,6 +680,12 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
       const bool whole = g.whole;
       float* part = a.prompt_part + static_cast<int64_t>(2 * blockIdx.x + (g.first ? 1 : 0)) * kPromptPartFloats;
       const int64_t orow = static_cast<int64_t>(g.q0 + tok) * a.Hq + g.h * group + at.y;
+      uint32_t nans = 0;                                 // bit b: the row sees a NaN in V channels 16 b ..
+      {
+        const volatile int* first = reinterpret_cast<const volatile int*>(sm + L::OFF_NAN) + (seg % L::NSEG) * 8;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) nans |= (first[b] <= tok - g.n ? 1u : 0u) << b;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + seg % L::NSEG);
       const float f = l == 0.f ? 0.f : *a.c.v_ts / l;
@@ -680,6 +698,11 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        if (nans) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (nans >> ((c + k) >> 4) & 1) o[k] = 0x7FFFFFFF;
         }
         if (real && whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * kKv4D + c);

@@ -34,6 +34,7 @@
 // Measured: 64 sequences of 8192 to 32768 tokens, 32 query and 8 KV heads, one token each: 273 us with the
 // join, 5.6 TB/s (86 % of the measured 6.5); one sequence of 1001 tokens: 12 us, two launches.
 #pragma once
+#include <climits>
 #include <type_traits>
 #include "kv4.cuh"
 #include "attn_fwd.cuh"
@@ -339,6 +340,7 @@ kv4_split_kernel(Kv4AttnArgs a) {
             *reinterpret_cast<const uint4*>(sm + L::OFF_Q + (nt * 8 + c) * L::Q_LD + t * 64 + k * 16);
     float2 m[NT], l[NT];
     float o[NT][8][4];
+    int nan_at = INT_MAX;                               // the first key with a NaN in this thread's V channels
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = make_float2(-INFINITY, -INFINITY);
@@ -442,10 +444,18 @@ kv4_split_kernel(Kv4AttnArgs a) {
             const uint4 vb = *reinterpret_cast<const uint4*>(sp + L::OFF_V + (r0 + 4) * 128 + c * 16);
             uint32_t sca = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + r0 * 2);
             uint32_t scb = *reinterpret_cast<const uint16_t*>(sp + L::OFF_VS + c * 64 + (r0 + 4) * 2);
-            if (p * 64 + 64 > g.q.ctx) {                   // slots behind the context: weight 0, value 0
+            if (p * 64 + 63 > g.q.ctx - g.q.n) {           // slots behind the context: weight 0, value 0
               const int left = g.q.ctx - p * 64;           // valid slots of the page
               if (2 * r0 >= left) sca = 0; else if (2 * r0 + 1 >= left) sca &= 0xFFu;
               if (2 * r0 + 8 >= left) scb = 0; else if (2 * r0 + 9 >= left) scb &= 0xFFu;
+              // A NaN would reach the rows that do not see it too (0 x NaN): value 0, and NaN for those that do in the end
+              const uint32_t na = e4m3_nans(sca), nb = e4m3_nans(scb);
+              if (na | nb) {
+                const int at = na ? 2 * r0 + ((na & 0x80u) ? 0 : 1) : 2 * r0 + 8 + ((nb & 0x80u) ? 0 : 1);
+                nan_at = min(nan_at, p * 64 + at);
+                sca &= ~((na >> 7) * 0xFFu);
+                scb &= ~((nb >> 7) * 0xFFu);
+              }
             }
             const __half2 fa = e4m3x2_to_half2(sca), fb = e4m3x2_to_half2(scb);
             const uint32_t* vaw = reinterpret_cast<const uint32_t*>(&va);
@@ -481,6 +491,18 @@ kv4_split_kernel(Kv4AttnArgs a) {
     // ---- the warps' results joined, eight rows at a time ----
     const bool whole = g.p0 == 0 && g.p1 == g.np;
     float* mbuf = reinterpret_cast<float*>(ring + (st ^ 1) * L::STAGE);
+    if (__any_sync(0xffffffffu, nan_at != INT_MAX)) {
+#pragma unroll
+      for (int x = 1; x <= 2; x <<= 1) nan_at = min(nan_at, __shfl_xor_sync(0xffffffffu, nan_at, x));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (nan_at <= row_lim[nt * 8 + 2 * t + k]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[nt][i][k] = o[nt][i][2 + k] = __int_as_float(0x7FFFFFFF);
+          }
+    }
     int* at = reinterpret_cast<int*>(sm + L::OFF_AT);
     if (lane == 0) at[warp] = owed ? static_cast<int>(reinterpret_cast<unsigned char*>(mbuf) - sm) : -1;
     float2* mlbuf = reinterpret_cast<float2*>(sm + L::OFF_ML);

@@ -465,6 +465,8 @@ qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream)
  * (append them first). Query head h reads KV head h / (q_heads / kv_heads). Neither the queries
  * nor the weights are quantized: q keeps its 16 bits, K and V their cached values, scores,
  * running maxima and sums are FP32, and the weights enter P V as fp16 scaled by 2^6.
+ * A cached NaN reaches the queries that see its token and no others: from K their whole rows, from
+ * V the 16 channels of its scale.
  * Rows at or past cu_q[S] of out (and lse) are left as they were. total_q may be 0 (q and out
  * are not looked at then).
  * Device checks, each setting QK4V8_ERR_BOUNDS: n_s outside [0, max_q], cu_q[s] or cu_q[s+1]

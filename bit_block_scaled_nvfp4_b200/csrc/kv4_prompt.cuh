@@ -586,6 +586,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
+      if (somebodys) C = kv4_score_factor(C);
       const int lim_min = g.ctx - g.n + t0 - g.j0 * 128; // the last key that every row of the unit sees, from the segment's first
       float m_ref = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

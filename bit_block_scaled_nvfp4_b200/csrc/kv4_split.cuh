@@ -233,6 +233,11 @@ __device__ __forceinline__ float2 kv4_row_factor(float amax) {
                      __uint_as_float(static_cast<uint32_t>(127 + e) << 23));
 }
 
+// A row's factor from products to scores in base 2. One that has left FP32's range at the bottom becomes the
+// smallest normal number: products stay below 2^35, so every score is still as good as 0, while 0 times a hidden
+// key's -inf would be NaN.
+__device__ __forceinline__ float kv4_score_factor(float c) { return c == 0.f ? 0x1p-126f : c; }
+
 template <int NT, typename T>
 __global__ void __launch_bounds__(Kv4SplitLayout<NT>::THREADS, 1)
 kv4_split_kernel(Kv4AttnArgs a) {
@@ -325,7 +330,7 @@ kv4_split_kernel(Kv4AttnArgs a) {
       *reinterpret_cast<uint2*>(sm + L::OFF_Q + r * L::Q_LD + lane * 8) =
           make_uint2(pack_half2(f[0] * fac.x, f[1] * fac.x), pack_half2(f[2] * fac.x, f[3] * fac.x));
       if (lane == 0) {
-        row_c[r] = fac.y * (*a.c.k_ts * a.softmax_scale * kLog2e);
+        row_c[r] = kv4_score_factor(fac.y * (*a.c.k_ts * a.softmax_scale * kLog2e));
         row_lim[r] = r < rows ? g.q.ctx - g.q.n + r / group : -1;
       }
     }

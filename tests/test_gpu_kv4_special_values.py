@@ -1,6 +1,7 @@
-"""GPU: attention over the 4-bit cache where a cached value is NaN. A query's output is a function of the keys it
-sees alone, so a NaN behind them changes no bit of it; where it sees the NaN the formula says which outputs are NaN:
-those of a V block's 16 channels, or all of a row's for a key."""
+"""GPU: attention over the 4-bit cache where a cached value is NaN, and where scores vanish. A query's output is a
+function of the keys it sees alone, so a NaN behind them changes no bit of it; where it sees the NaN the formula says
+which outputs are NaN: those of a V block's 16 channels, or all of a row's for a key. Scores: tolerances as derived in
+test_gpu_kv4_attention.py."""
 import math
 
 import pytest
@@ -76,3 +77,13 @@ def test_a_nan_key_reaches_the_queries_that_see_it_and_no_others(kind, dtype):
         bad[seen_by(c, s, pos), h * g:(h + 1) * g] = True
         assert got[bad].isnan().all() and got_lse[bad].isnan().all(), (s, pos)
         assert torch.equal(got[~bad], out[~bad]) and torch.equal(got_lse[~bad], lse[~bad]), (s, pos)
+
+
+@kinds
+@pytest.mark.parametrize("dtype,q_scale,scale", [(torch.bfloat16, 2.0 ** -120, 2.0 ** -24), (torch.bfloat16, 1.0, 2.0 ** -146),
+                                                 (torch.float16, 1.0, 2.0 ** -146)])
+def test_scores_too_small_for_float32_are_zero(kind, dtype, q_scale, scale):
+    """The factor from products to scores leaves float32's range at the bottom: every key that a row sees has
+    the same weight, the others none."""
+    c = Case(*KINDS[kind], dtype, seed=23, q_scale=q_scale)
+    c.check(*c.run(softmax_scale=scale), scale=scale)

@@ -807,7 +807,8 @@ def _pool_workspace(pool, page_table):
 def kv_pages_alloc(pool, page_table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor) -> None:
     """Give every sequence the pages it needs to grow from lens[s] to new_lens[s] tokens, lowest
     free pages first (page_table and pool.refs updated in place; lens is not: append, then
-    advance it). All or nothing: see kv_pages_alloc in include/qk4v8.h."""
+    advance it). All or nothing: see kv_pages_alloc in include/qk4v8.h, which also says how tokens
+    are taken back (lens never falls but by kv_pages_free)."""
     args = _pool_args(pool, page_table, lens, ("new_lens", new_lens))
     if new_lens.numel() != lens.numel():
         raise ValueError("new_lens must have one entry per sequence")

@@ -86,6 +86,10 @@ pages_alloc_kernel(int32_t* refs, int P, int32_t* table, int S, int max_pages,
       const int n0 = lens[s], n1 = new_lens[s];
       if (n0 < 0 || n1 < n0 || pool_pages_of(n1) > max_pages) bad = true;
       else need = pool_pages_of(n1) - pool_pages_of(n0);
+      if (!bad && n1 > n0 && (n0 & 63) != 0) {           // tokens will be stored into its last page: it has to be its own
+        const int id = table[static_cast<int64_t>(s) * max_pages + (n0 >> 6)];
+        if (id >= 0 && id < P && refs[id] > 1) bad = true;
+      }
     }
     // 2^20 pages more for one sequence are refused as well: 1024 of them would pass 32 bits
     if (need > P || need >= 1 << 20) { bad = true; need = 0; }

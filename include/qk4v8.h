@@ -399,8 +399,9 @@ qk4v8_status kv_append_paged(const qk4v8_append_params* params, cudaStream_t str
 /*
  * The 4-bit paged cache: K and V both in NVFP4 (E2M1 codes, one E4M3 scale per 16 channels of a
  * token, one FP32 scale per tensor; the quantize_nvfp4 arithmetic with a fixed tensor scale).
- * Every token is quantized on its own, so a cache can be appended to, cut back and forked at any
- * token and needs no state besides its pages. 144 bytes a token and KV head at head_dim 128.
+ * Every token is quantized on its own, so a sequence can be appended to and forked at any token,
+ * and overwritten from any token on, and needs no state besides its pages (whose pages a pool manages:
+ * its rule for taking tokens back is below). 144 bytes a token and KV head at head_dim 128.
  * Pages hold 64 tokens:
  *   k_pages       [num_pages, Hkv, 64, D/2]   channel 2i of a token in the low nibble of byte i
  *   k_page_scales [num_pages, Hkv, 64, D/16]
@@ -508,8 +509,17 @@ qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* params, void* workspace
  * A call whose arguments cannot be met as a whole (a sequence id out of range, too few free
  * pages, a length past 64 * max_pages, ...) changes nothing and sets QK4V8_ERR_BOUNDS.
  *
+ * lens[s] falls by kv_pages_free alone. The pool knows a sequence's pages by its length: pages behind a
+ * length that a caller lowers belong to nobody and do not come back. To take tokens back (refused
+ * proposals), keep lens at what has been allocated and the tokens' own lengths beside it, for the cache's
+ * append and the attention; the next kv_pages_alloc goes from lens to the larger of lens and the new
+ * length. With m = 64 * (lens[s] / 64) rounded down when s is forked: its own length has to be
+ * at least m then, and neither s nor its fork takes tokens back below m while the other lives
+ * (the pages before m are both's; kv_pages_alloc sees that only where lens itself ends inside one).
+ *
  * kv_pages_alloc    pages for growing from lens[s] to new_lens[s] (>= lens[s]) tokens, for every
- *                   s; lens is not modified (append, then advance it).
+ *                   s; lens is not modified (append, then advance it). Refused where a sequence would
+ *                   grow into a last page that other sequences hold too.
  * kv_pages_fork     sequence src[i] forked into the empty sequence dst[i] (lens[dst] == 0; all
  *                   dst distinct, none its own src), i < n: full pages are shared, a last page that is not
  *                   full is to be copied into a page of dst's own. Writes the copies to make to

@@ -220,12 +220,39 @@ pages_free_kernel(int32_t* refs, int P, int32_t* table, int S, int max_pages, in
   }
 }
 
-// ws: n_live [1], holes [P], map [P]. move_src / move_dst have P / 2 + 1 entries: a move fills a
+// Whether each sequence's length fits its row and its pages exist and are held, for the compaction that
+// follows: bad [S]. One CTA per sequence.
+__global__ void __launch_bounds__(128)
+pages_check_kernel(const int32_t* refs, int P, const int32_t* table, int max_pages, const int32_t* lens,
+                   int32_t* bad) {
+  const int s = blockIdx.x, len = lens[s];
+  bool wrong = len < 0 || pool_pages_of(len) > max_pages;
+  const int np = wrong ? 0 : pool_pages_of(len);
+  for (int p = threadIdx.x; p < np; p += blockDim.x) {
+    const int id = table[static_cast<int64_t>(s) * max_pages + p];
+    if (id < 0 || id >= P || refs[id] <= 0) wrong = true;
+  }
+  wrong = __syncthreads_or(wrong);
+  if (threadIdx.x == 0) bad[s] = wrong;
+}
+
+// ws: n_live [1] (-1: refused), bad [S], holes [P], map [P]. move_src / move_dst have P / 2 + 1 entries: a move fills a
 // hole, so there are no more moves than live pages and no more than holes.
 __global__ void __launch_bounds__(kPoolThreads)
-pages_compact_kernel(int32_t* refs, int P, int32_t* move_src, int32_t* move_dst,
-                     int32_t* move_count, int32_t* n_live_out, int32_t* holes, int32_t* map) {
+pages_compact_kernel(int32_t* refs, int P, int S, int32_t* move_src, int32_t* move_dst, int32_t* move_count,
+                     int32_t* n_live_out, const int32_t* bad, int32_t* holes, int32_t* map) {
   __shared__ int sh[33];
+  bool wrong = false;
+  for (int s = threadIdx.x; s < S; s += kPoolThreads) wrong |= bad[s] != 0;
+  if (__syncthreads_or(wrong)) {
+    for (int i = threadIdx.x; i < P / 2 + 1; i += kPoolThreads) move_src[i] = move_dst[i] = -1;
+    if (threadIdx.x == 0) {
+      *move_count = 0;
+      *n_live_out = -1;
+      flag_error(kStatusBounds);
+    }
+    return;
+  }
   int live = 0;
   for (int base = 0; base < P; base += kPoolThreads * 4) {
     const int p = base + threadIdx.x * 4;
@@ -270,21 +297,17 @@ pages_compact_kernel(int32_t* refs, int P, int32_t* move_src, int32_t* move_dst,
   }
 }
 
-// Page-table entries of moved pages. One CTA per sequence.
+// Page-table entries of moved pages (all checked before anything moved). One CTA per sequence.
 __global__ void __launch_bounds__(128)
 pages_remap_kernel(int P, int32_t* table, int max_pages, const int32_t* lens, const int32_t* n_live,
                    const int32_t* map) {
-  const int s = blockIdx.x, len = lens[s], live = *n_live;
-  if (len < 0 || pool_pages_of(len) > max_pages) {
-    if (threadIdx.x == 0) flag_error(kStatusBounds);
-    if (len < 0) return;
-  }
-  const int np = min(pool_pages_of(len), max_pages);
+  const int s = blockIdx.x, live = *n_live;
+  if (live < 0) return;
+  const int np = min(pool_pages_of(lens[s]), max_pages);
   for (int p = threadIdx.x; p < np; p += blockDim.x) {
     const int64_t e = static_cast<int64_t>(s) * max_pages + p;
     const int id = table[e];
-    if (id < 0 || id >= P || (id >= live && map[id] < 0)) flag_error(kStatusBounds);
-    else if (id >= live) table[e] = map[id];
+    if (id >= live && id < P) table[e] = map[id];
   }
 }
 

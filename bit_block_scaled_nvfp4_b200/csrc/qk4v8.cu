@@ -1053,9 +1053,13 @@ extern "C" qk4v8_status kv_pages_compact(int32_t* refs, int32_t num_pages, int32
   if (st != QK4V8_OK) return st;
   if (!move_src || !move_dst || !move_count) return QK4V8_ERR_INVALID_ARG;
   int32_t* n_live = static_cast<int32_t*>(workspace);
+  int32_t* bad = n_live + 1;
   int32_t* holes = n_live + num_seqs + 2;
   int32_t* map = holes + num_pages;
-  pages_compact_kernel<<<1, kPoolThreads, 0, stream>>>(refs, num_pages, move_src, move_dst, move_count, n_live, holes, map);
+  pages_check_kernel<<<num_seqs, 128, 0, stream>>>(refs, num_pages, page_table, max_pages, lens, bad);
+  if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
+  pages_compact_kernel<<<1, kPoolThreads, 0, stream>>>(refs, num_pages, num_seqs, move_src, move_dst, move_count, n_live,
+                                                       bad, holes, map);
   if (launch_status() != QK4V8_OK) return QK4V8_ERR_CUDA;
   pages_remap_kernel<<<num_seqs, 128, 0, stream>>>(num_pages, page_table, max_pages, lens, n_live, map);
   return launch_status();

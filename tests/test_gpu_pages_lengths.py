@@ -11,6 +11,27 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.status_checked
+@pytest.mark.parametrize("fault", ["negative length", "length past the table", "no such page", "negative page", "page that nobody holds"])
+@pytest.mark.parametrize("seqs", [4, 300])
+def test_refused_compactions_change_nothing(fault, seqs):
+    p = Pair(5 * seqs, seqs, 4)
+    p.grow([200 - s % 70 for s in range(seqs)])
+    p.free(list(range(0, seqs, 2)))
+    bad = seqs - 1                                        # the last row, with rows to move before it
+    if "length" in fault:
+        p.lens[bad] = -1 if fault == "negative length" else 257
+    else:
+        free = int((p.pool.refs == 0).nonzero()[0])
+        p.table[bad, 1] = {"no such page": 5 * seqs, "negative page": -1, "page that nobody holds": free}[fault]
+    before = _state(p)
+    api.check_status()
+    moves = api.kv_pages_compact(p.pool, p.table, p.lens)
+    assert api.check_status() == 5
+    assert all(torch.equal(a, b) for a, b in zip(_state(p), before))
+    assert int(moves.count) == 0 and (moves.src == -1).all() and (moves.dst == -1).all()
+
+
+@pytest.mark.status_checked
 @pytest.mark.parametrize("cut,new", [(100, 101), (100, 130), (127, 128), (1, 400)])
 def test_a_page_that_two_sequences_hold_is_not_given_for_appending(cut, new):
     """A fork cut back into a page it shares: what it would append there is another sequence's."""

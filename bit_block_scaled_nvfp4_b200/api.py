@@ -852,6 +852,10 @@ def kv_pages_compact(pool, page_table: torch.Tensor, lens: torch.Tensor) -> Page
 
 
 def _copy_rows(arrays, src, dst, rows: int, count) -> None:
+    _expect(src, "moves.src", (src.numel(),), torch.int32)
+    _expect(dst, "moves.dst", (src.numel(),), torch.int32)
+    if count is not None:
+        _expect(count, "moves.count", (1,), torch.int32)
     _on_one_gpu(*arrays, src, dst, count)
     n = len(arrays)
     ptrs = (C.c_void_p * n)(*[a.data_ptr() for a in arrays])

@@ -26,16 +26,19 @@ def _stream():
     return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _launch(name: str, dev: int, *args) -> None:
-    """One call of the library on device ``dev`` and its current stream (entering the device costs more
-    than many a call's own checks, so only when it is not the current one)."""
-    fn, stream = getattr(_lib.load(), name), torch.cuda.current_stream(dev).cuda_stream
+def _on_device(name: str, dev: int, *args):
+    """One call of the library with device ``dev`` current (entering it costs more than many a call's
+    own checks, so only when it is not)."""
+    fn = getattr(_lib.load(), name)
     if torch.cuda.current_device() == dev:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
-    _lib.check(st, name)
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _launch(name: str, dev: int, *args) -> None:
+    """One call of the library on device ``dev`` and its current stream."""
+    _lib.check(_on_device(name, dev, *args, torch.cuda.current_stream(dev).cuda_stream), name)
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -691,7 +694,7 @@ def _kv4_attn_params(q: torch.Tensor, cache: PagedKV4, page_table: torch.Tensor,
 
 
 def _kv4_workspace(p, workspace, device):
-    need = _lib.load().attn_kv4_paged_workspace_size(C.byref(p))
+    need = _on_device("attn_kv4_paged_workspace_size", device.index, C.byref(p))   # it goes with the device's SMs
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or workspace.numel() < need:
@@ -745,8 +748,7 @@ class KV4AttentionPlan:
         probe_cu = torch.empty(S + 1, dtype=torch.int32, device=dev)
         self.params = _kv4_attn_params(self.out, cache, page_table, context_lens, max_context, probe_cu,
                                        max_q, softmax_scale, self.out, self.lse)
-        with torch.cuda.device(dev):
-            self.workspace = _kv4_workspace(self.params, workspace, dev)
+        self.workspace = _kv4_workspace(self.params, workspace, dev)
         self._keep = (cache, page_table, context_lens)
         self._shape, self._dtype = (q_heads, d), dtype
         self._dev = self.out.get_device()

@@ -474,8 +474,9 @@ qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream)
  * outside [0, total_q], or a context outside [n_s, min(max_context, 64 * max_pages)] (the
  * sequence's rows are left as they were); a page id outside [0, num_pages) (that page's keys
  * are left out; a row with no key left gets O = 0 and lse = -inf).
- * workspace  >= attn_kv4_paged_workspace_size(params) bytes, 16-byte aligned; its contents
- *            before and after mean nothing, calls that may overlap need one each.
+ * workspace  >= attn_kv4_paged_workspace_size(params) bytes (asked with the call's device current: the
+ *            size goes with its SMs), 16-byte aligned; its contents before and after mean
+ *            nothing, calls that may overlap need one each.
  */
 typedef struct {
   qk4v8_kv4_cache cache;

@@ -1,4 +1,7 @@
-"""Host-side checks of the page pool's calls, without a GPU: move lists that do not belong together."""
+"""Host-side checks of the 4-bit cache's and the page pool's calls, without a GPU: move lists that do not
+belong together, and the device a workspace is sized for."""
+import contextlib
+
 import pytest
 import torch
 
@@ -21,3 +24,27 @@ def test_page_copies_check_their_lists(src, dst, count, error, what):
     if count is None:
         with pytest.raises(error, match=what):
             api.kv_tails_copy(torch.zeros(4, 1, 128, 32), api.PageMoves(i32(3), i32(3), 30, None, src, dst))
+
+
+def test_the_workspace_is_sized_for_the_tensors_device(monkeypatch):
+    """Its size goes with the device's SMs: the library answers for the current device, so the tensors' is entered."""
+    entered, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(torch.device("cuda", d).index if isinstance(d, int) else d.index)
+        yield
+        entered.pop()
+
+    class Lib:
+        @staticmethod
+        def attn_kv4_paged_workspace_size(p):
+            asked.append(entered[-1])
+            return 64
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: entered[-1])
+    monkeypatch.setattr(api._lib, "load", lambda: Lib)
+    with pytest.raises(ValueError):                       # (no GPU here: the workspace is refused after that)
+        api._kv4_workspace(api._lib.Kv4AttnParams(), torch.empty(64, dtype=torch.uint8), torch.device("cuda", 1))
+    assert asked == [1] and entered == [0]

@@ -732,7 +732,8 @@ class KV4AttentionPlan:
     outputs for up to ``max_tokens`` query tokens, workspace) are checked and allocated once;
     ``run(q, cu_q)`` checks the step's queries and launches, and returns views of the plan's own
     outputs (read them before the next ``run``). Steps that may overlap, on two streams or in two
-    graphs, need a plan each: outputs and workspace are the plan's."""
+    graphs, need a plan each: outputs and workspace are the plan's. ``max_q`` also chooses the
+    kernels: single-token steps are faster under a plan of their own than under a prompt's."""
 
     def __init__(self, cache: PagedKV4, page_table: torch.Tensor, context_lens: torch.Tensor,
                  max_context: int, q_heads: int, max_q: int = 1, max_tokens: int | None = None,

@@ -15,8 +15,8 @@
 // The key tiles of all items form one line, cut into equal ranges, one a CTA (kv4_range), whatever
 // the lengths and however few the rows; an item that crosses CTAs leaves partials.
 //
-// Measured, 32 query and 8 KV heads: 16384 tokens 2.17 ms (1.01 PFLOP/s, 61 % of the measured bf16 rate), 512 tokens
-// after 32000 cached 280 us (0.97 PFLOP/s). A tile of two units takes about 3900 cycles: the
+// Measured as graphs, 32 query and 8 KV heads: 16384 tokens 2.19 ms (1.00 PFLOP/s, 61 % of the measured bf16 rate), 512
+// tokens after 32000 cached 279 us (0.97 PFLOP/s). A tile of two units takes about 3900 cycles: the
 // softmax warps are busy for 1690 of a half tile's 1930 (exponentials of two warps an SM quarter, 1024, behind them
 // the maximum, the packing and the decoding warps' share of the issue slots). With one unit of rows (a few proposed
 // tokens) a tile still takes about 3300: the decoding of its pages, by one pair of warps for K and one for V, is then
@@ -37,7 +37,8 @@ namespace qk4v8 {
 constexpr float kRiseLimit = 8.f;                        // log2 of how far the maximum may rise unfollowed
 constexpr int kPromptPartFloats = 256 * (kKv4D + 2);     // a partial: O, then m, then l of 256 rows
 
-// sum over i < n of floor((a i + b) / 128), n < 2^31, by the steps of Euclid's algorithm on (a, 128). Divisions are in
+// sum over i < n of floor((a i + b) / 128), n < 2^31: the published floor-sum algorithm (whole parts taken out, then
+// the roles of a and the modulus exchanged, as Euclid's algorithm goes on (a, 128)). Divisions are in
 // 32 bits where the numbers allow it: 64-bit ones made the search for a CTA's place take 10 us.
 __device__ __forceinline__ int64_t floor_sum128(uint32_t n, uint32_t a, uint64_t b64) {
   uint32_t m = 128, b = static_cast<uint32_t>(b64 & 127);

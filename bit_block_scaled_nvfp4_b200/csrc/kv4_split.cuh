@@ -5,11 +5,13 @@
 // head of the group) see the same keys. S^T = K Q^T and O^T += V^T P^T on 16-bit tensor cores with
 // FP32 accumulators; K and V are E2M1 x E4M3 products of at most six significant bits between
 // 2^-10 and 2688, exact in fp16. Q is scaled per row by a power of two into fp16's range (exact
-// but for elements 2^-20 below the row's largest) and the factor goes into the softmax constant.
-// P = 2^(s - m + 6) is rounded to fp16 (2^-12 relative; the 2^6 keeps weights down to 2^-20
+// but for elements more than 2^27 times below the row's largest) and the factor goes into the softmax constant.
+// P = 2^(s - m + 6) is rounded to fp16 (2^-11 relative; the 2^6 keeps weights down to 2^-20
 // of the largest out of the subnormals); m, l and O are FP32, l sums the unrounded weights.
 //
-// Bound: the cache is read once, 144 bytes a token and KV head, and everything is laid out so
+// Bound: with up to eight rows a KV head, HBM: the cache is read once, 144 bytes a token and KV head. With 9 to 16
+// rows (NT = 2) it is not: 24 sequences of two tokens of 8 heads take 95 us, 21 % of the HBM rate, with half the tokens
+// in flight and twice the softmax and products for each decoded word. Everything is laid out so
 // that codes go from shared memory into tensor-core operands without being moved between threads:
 //   * keys are the M dimension of both products (16 tokens or 16 channels a tile), rows the N
 //     dimension (8 a tile), so a decoding step of g <= 8 wastes nothing on padding rows to 16;
@@ -31,8 +33,9 @@
 // by 16-byte asynchronous copies, with no barrier between warps until a pair ends. (One warp
 // issuing bulk copies for all of them reached 1 page in 1020 cycles, 4 copies of 4096 + 4096 +
 // 512 + 512 bytes: 33 % of the HBM rate.)
-// Measured: 64 sequences of 8192 to 32768 tokens, 32 query and 8 KV heads, one token each: 273 us with the
-// join, 5.6 TB/s (86 % of the measured 6.5); one sequence of 1001 tokens: 12 us, two launches.
+// Measured as graphs: 64 sequences of 8192 to 32768 tokens, 32 query and 8 KV heads, one token each: 274 us with
+// the join, 5.6 TB/s (86 % of the measured 6.5; planned calls whose inputs change from pass to pass: 295 to 312 us); one
+// sequence of 1001 tokens: 12 us, two launches.
 #pragma once
 #include <climits>
 #include <type_traits>

@@ -4,12 +4,14 @@
 // function of the state and the arguments, whatever order the threads run in.
 //
 // The planning steps need one consistent view of refs and lens, so each is one CTA: a pass over
-// refs (4 bytes a page, 64 pages a warp-wide 16-byte load) and block scans. Work that grows with
-// the bytes moved (page contents, page tables) runs over the whole device.
+// refs (4 bytes a page, 128 pages a warp-wide 16-byte load) and block scans; a fork's table rows are
+// checked and copied by that CTA too, so its time grows with forks times the table's width. Page contents and the
+// tables of freed and compacted sequences are spread over the device.
 //
-// Measured on the device: 64 sequences of 200 to 4000 tokens freed and forked again, their last pages copied:
+// Measured as graphs: 64 sequences of 200 to 4000 tokens freed and forked again, their last pages copied:
 // 17 us, three launches and the one CTA's passes (the bytes alone: 1.3 us); 48 sequences of 500 to 5000 tokens
-// compacted among three times as many pages, contents of 8 heads copied: 52 us, of which the copies' bytes are 32.
+// compacted among three times as many pages, contents of 8 heads copied: 55 us, four launches, of which the copies'
+// bytes are 32 (52 us before the rows were checked in a launch of their own).
 #pragma once
 #include "ptx.cuh"
 
@@ -46,7 +48,7 @@ __device__ __forceinline__ int block_scan(int v, int* sh, int& total) {
   return sh[warp] + x - v;
 }
 
-// Four refs from page p on; pages past the end read as 1 when `past_end_used`, else 0.
+// Four refs from page p on; pages past the end read as `past`.
 __device__ __forceinline__ int4 load_refs(const int32_t* refs, int P, int p, int past) {
   if (p + 3 < P && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) return *reinterpret_cast<const int4*>(refs + p);
   return make_int4(p < P ? refs[p] : past, p + 1 < P ? refs[p + 1] : past, p + 2 < P ? refs[p + 2] : past,

@@ -863,10 +863,11 @@ struct Kv4Schedule {
 };
 // Where every sequence has at most 16 rows a KV head (query tokens times heads a group) the split
 // kernel takes them all: 24 sequences of 2 tokens x 8 heads a group at 700 to 9000 cached take 95 us, by
-// the prompt kernel 120. From 17 rows on the prompt kernel is the faster one (an instance of the split
-// kernel for 32 rows: 3 tokens 142 us against 122, 128 short sequences 180 against 84, two short ones 29
-// against 31). It then leaves the sequences of one token (of a whole tile of rows, to be exact) to the split kernel;
-// a lone sequence is the prompt kernel's whatever its length, which saves the other's two launches.
+// the prompt kernel 120. From 17 rows on the prompt kernel takes them: against an instance of the split
+// kernel for 32 rows it was the faster one but for very few short sequences (3 tokens 122 us against 142, 128 short
+// sequences 84 against 180, two short ones 31 against 29). It then leaves the sequences of one token (of a whole tile of rows, to be exact) to the split kernel;
+// a lone sequence is the prompt kernel's whatever its length, which saves the other's two launches. The rule knows
+// max_q, the host's bound, and not the tokens there are: steps are best planned with a bound of their own.
 Kv4Schedule kv4_schedule(const qk4v8_kv4_attn_params* p) {
   Kv4Schedule s;
   const int64_t group = p->q_heads / p->cache.kv_heads, rows = p->max_q * group;

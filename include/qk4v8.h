@@ -470,8 +470,8 @@ qk4v8_status kv4_read_paged(const qk4v8_kv4_tokens* params, cudaStream_t stream)
  * V the 16 channels of its scale.
  * Rows at or past cu_q[S] of out (and lse) are left as they were. total_q may be 0 (q and out
  * are not looked at then).
- * Device checks, each setting QK4V8_ERR_BOUNDS: n_s outside [0, max_q], cu_q[s] or cu_q[s+1]
- * outside [0, total_q], or a context outside [n_s, min(max_context, 64 * max_pages)] (the
+ * Device checks, each setting QK4V8_ERR_BOUNDS: n_s outside [0, max_q], or, of a sequence with
+ * query tokens, cu_q[s] or cu_q[s+1] outside [0, total_q] or a context outside [n_s, max_context] (the
  * sequence's rows are left as they were); a page id outside [0, num_pages) (that page's keys
  * are left out; a row with no key left gets O = 0 and lse = -inf).
  * workspace  >= attn_kv4_paged_workspace_size(params) bytes (asked with the call's device current: the
@@ -489,9 +489,10 @@ typedef struct {
   const int32_t* page_table;   /* [S, max_pages] */
   int32_t num_seqs, max_pages;
   int32_t q_heads;             /* a multiple of kv_heads, at most 16 times it */
-  int32_t max_q;               /* host-side bound on n_s */
-  int32_t max_context;         /* host-side bound on context_lens */
-  float softmax_scale;
+  int32_t max_q;               /* host-side bound on n_s; it also chooses the kernels, so calls for steps
+                                  alone are faster with 1 than with a prompt's length */
+  int32_t max_context;         /* host-side bound on context_lens, <= 64 * max_pages */
+  float softmax_scale;         /* > 0 */
   void* out;                   /* [total_q, Hq, D] contiguous, 16-byte aligned, apart from q */
   float* lse;                  /* optional [total_q, Hq] natural-log sum-exp; or NULL */
 } qk4v8_kv4_attn_params;
@@ -520,7 +521,8 @@ qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* params, void* workspace
  *
  * kv_pages_alloc    pages for growing from lens[s] to new_lens[s] (>= lens[s]) tokens, for every
  *                   s; lens is not modified (append, then advance it). Refused where a sequence would
- *                   grow into a last page that other sequences hold too.
+ *                   grow into a last page that other sequences hold too, and where one grows by 2^20
+ *                   pages or more.
  * kv_pages_fork     sequence src[i] forked into the empty sequence dst[i] (lens[dst] == 0; all
  *                   dst distinct, none its own src), i < n: full pages are shared, a last page that is not
  *                   full is to be copied into a page of dst's own. Writes the copies to make to
@@ -529,7 +531,8 @@ qk4v8_status attn_kv4_paged(const qk4v8_kv4_attn_params* params, void* workspace
  *                   seq_src / seq_dst [n] (-1 everywhere when the call is refused).
  * kv_pages_free     sequences seqs[i] dropped: their pages' counts fall, their row entries become -1
  *                   and lens 0. A sequence that is empty, or named twice, is freed once. An id
- *                   or page out of range, or a page nobody holds, is skipped (QK4V8_ERR_BOUNDS).
+ *                   or page out of range, a page nobody holds and the part of a length past the table
+ *                   are skipped (QK4V8_ERR_BOUNDS).
  * kv_pages_compact  live pages moved into [0, number of live pages): the i-th live page past
  *                   that goes to the i-th hole before it. Page tables and refs follow; the moves are
  *                   written to move_src / move_dst [num_pages / 2 + 1] and their number to

@@ -544,6 +544,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, Kv4AttnArgs a) {
       p1 = p2;
       p2 = p3;
     }
+    cp_async_wait<0>();                                  // a wait that gave up leaves copies on their way
   } else {
     // ================================ softmax ================================
     const int wq = warp & 3, unit = (warp - 8) >> 2, row = wq * 32 + lane;

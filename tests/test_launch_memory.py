@@ -1,6 +1,6 @@
-"""Shared memory of the kernels that move their base up to the next 1024 bytes themselves (CPU, from
-the source): what such a kernel is launched with, and opted in for, has to hold its layout behind the
-largest move, or its barriers lie behind the allocation wherever the base is not aligned by itself."""
+"""Shared memory of launches and of early ends (CPU, from the source). What a kernel that moves its base up to the
+next 1024 bytes is launched with, and opted in for, has to hold its layout behind the largest move, or its
+barriers lie behind the allocation wherever the base is not aligned by itself."""
 import os
 import re
 
@@ -42,3 +42,14 @@ def test_kernels_that_align_their_base_are_launched_with_the_room_for_it():
 def test_the_room_holds_the_largest_move():
     for f in ("attn_fwd.cuh", "attn_pp.cuh", "decode.cuh"):
         assert re.search(r"SMEM_ALLOC = SMEM_BYTES \+ 1024;", _source(f)), f
+
+
+def test_no_role_of_the_prompt_kernel_leaves_copies_on_their_way():
+    """A wait that gives up ends a role early: the decoding warps' copies into shared memory, and Q's, are waited
+    for behind their loops, whichever way these end."""
+    text = _source("kv4_prompt.cuh")
+    text = text[text.index("void __launch_bounds__(512, 1)"):]
+    queries, rest = text.split("K and V decoding", 1)
+    decoding = rest.split("= softmax =", 1)[0]
+    assert queries.rindex("mbar_wait(kConvertQ ? q_raw : q_full") > queries.rindex("tma_load_3d(")
+    assert "cp_async_wait<0>()" in decoding and decoding.rindex("cp_async_wait<0>()") > decoding.rindex("cp_async_commit()")
